@@ -115,6 +115,10 @@ typedef int32_t eq_status;
 
 #define EQ_DTYPE_INT8 1u /* two's-complement int8 codes */
 #define EQ_DTYPE_E4M3 2u /* OCP FP8 E4M3FN codes */
+#define EQ_DTYPE_INT4 3u /* 4-bit integer codes (eq_w4_*) */
+#define EQ_DTYPE_E2M1 4u /* OCP FP4 E2M1 codes: 0, .5, 1, 1.5, 2, 3, 4, 6 and their negatives */
+#define EQ_DTYPE_BF16 5u /* bf16 bit patterns (u16) */
+#define EQ_DTYPE_F32 6u  /* binary32 */
 
 #define EQ_CODEC_RANS 0u    /* container codec: interleaved rANS (EntQuant's ANS) */
 #define EQ_CODEC_HUFFMAN 1u /* container codec: interleaved canonical Huffman (EntroLLM) */
@@ -381,6 +385,124 @@ eq_status eq_pipeline_destroy(eq_pipeline *p);
  * checked over all 2^32 inputs. Errors: EQ_EINVAL, EQ_EHIP.
  */
 eq_status eq_bf16_from_f32(const float *d_in, uint64_t n, uint16_t *d_out, void *stream);
+
+/*
+ * The steps around a block's weight products (eq_add_rmsnorm, eq_silu_mul,
+ * eq_w4_matvec). They only enqueue kernels: no allocation, no workspace, no
+ * synchronisation; with zero tokens nothing is enqueued. Results do not
+ * depend on timing (no atomics; every sum has a fixed order).
+ *
+ * eq_matrix: [tokens, width] activations in device memory; row t starts
+ * `stride` elements after row t - 1 (stride >= width; outputs must not
+ * overlap themselves). Any element alignment is accepted; rows that start at
+ * multiples of 16 bytes are read and written fastest.
+ *
+ * 8-bit matrices (EQ_DTYPE_INT8, EQ_DTYPE_E4M3) have one fp32 scale per row:
+ * value[t, c] = code[t, c] * d_scale[t]. A call that writes one derives them
+ * from the fp32 result v of the row: a = max(max_c |v[t, c]|, 2^-96),
+ * d_scale[t] = a / L and code = round(v * (L / a)) with L = 127 (int8) or 448
+ * (E4M3FN), to nearest, ties to even. A row that holds an infinity or a NaN
+ * gets a scale that is one (its values are then not meaningful).
+ */
+typedef struct eq_matrix {
+    void *d;           /* device pointer to element [0, 0]; not written where it is an input */
+    uint64_t stride;   /* elements from one row to the next */
+    float *d_scale;    /* 8-bit types: one fp32 per row; otherwise NULL */
+    uint32_t dtype;    /* EQ_DTYPE_* */
+    uint32_t reserved; /* 0 */
+} eq_matrix;
+
+/*
+ * eq_add_rmsnorm -- per token: s = x + residual (rounded to residual_out's
+ * type and written there), out = s / sqrt(mean(s^2) + eps) * weight. Without
+ * a residual (residual and residual_out both NULL) s = x.
+ * x: F32 (what eq_gemv_bf16, eq_decode_gemv_bf16 and eq_w4_matvec write) or
+ *    BF16. residual, residual_out: F32 or BF16, both the same type;
+ *    residual_out may be the residual itself (same pointer and stride: the
+ *    sum in place). d_weight: `cols` values of weight_dtype (BF16 or F32), or
+ *    NULL for ones. out: BF16, INT8 or E4M3 (see eq_matrix); it must not
+ *    overlap any other argument.
+ * Arithmetic: s^2 summed in fp32; out = (s * weight) * (1 / sqrt(...)) in
+ *    fp32, rounded once.
+ * Errors: EQ_EINVAL (NULL, a type not listed, cols 0 or above 2^31 - 1,
+ *    tokens above 2^31 - 1, a stride below cols, only one of residual and
+ *    residual_out, a missing scale array, eps negative or NaN), EQ_EHIP.
+ */
+eq_status eq_add_rmsnorm(const eq_matrix *x, const eq_matrix *residual, const eq_matrix *residual_out,
+                         const void *d_weight, uint32_t weight_dtype, float eps, uint64_t tokens,
+                         uint64_t cols, const eq_matrix *out, void *stream);
+
+/*
+ * eq_silu_mul -- per element: out = gate / (1 + exp(-gate)) * up, in fp32,
+ * rounded once. gate, up: F32 or BF16, both the same type (two halves of one
+ * buffer are two matrices with its stride). out: BF16, INT8 or E4M3; it must
+ * not overlap the inputs.
+ * Errors: EQ_EINVAL (as eq_add_rmsnorm), EQ_EHIP.
+ */
+eq_status eq_silu_mul(const eq_matrix *gate, const eq_matrix *up, uint64_t tokens, uint64_t cols,
+                      const eq_matrix *out, void *stream);
+
+/*
+ * 4-bit weights. W[r, c] = (q[r, c] - zero[r, g]) * scale[r, g], g = c / group:
+ * INT4 codes with d_zeros are unsigned (0..15, zero 0..255); without, they are
+ * two's complement (-8..7) and zero is 0; E2M1 codes are 4-bit floats
+ * (no d_zeros). group is 32, 64 or 128; the last group of a row may be short.
+ *
+ * The kernels read the weights in tiles of 16 rows x 128 columns, which
+ * eq_w4_pack lays out once, when a model is loaded (row-major codes were read
+ * at 4.2-5.0 TB/s against 6.1-6.4 for tiles): tile (r / 16, c / 128) is 1 KiB
+ * at (r / 16 * ceil(cols / 128) + c / 128) * 1024, the 16 bytes of its row
+ * i and quarter k at (16 * k + i) * 16: four u32, word j holding columns
+ * 32 * j + 8 * k + (0..7), 4 bits each from bit 0 up, for E2M1 in the order
+ * 0 1 2 3 4 5 6 7, for INT4 0 2 4 6 1 3 5 7. Scales and zeros go the same
+ * way: entry ((tile) * 16 + i) * (128 / group) + group within the tile.
+ * Padding holds zeros.
+ */
+typedef struct eq_w4_tensor {
+    uint32_t dtype;           /* EQ_DTYPE_INT4 or EQ_DTYPE_E2M1 */
+    uint32_t group;           /* 32, 64 or 128 columns per scale */
+    uint64_t rows, cols;
+    void *d_codes;            /* eq_w4_codes_bytes() bytes, 16-byte aligned */
+    uint16_t *d_scales;       /* eq_w4_groups() bf16, 8-byte aligned */
+    uint8_t *d_zeros;         /* eq_w4_groups() bytes, 4-byte aligned, or NULL */
+} eq_w4_tensor;
+
+/* Sizes of the laid-out arrays (0 for invalid arguments). */
+uint64_t eq_w4_codes_bytes(uint64_t rows, uint64_t cols);
+uint64_t eq_w4_groups(uint64_t rows, uint64_t cols, uint32_t group);
+
+/*
+ * eq_w4_pack -- lays out row-major 4-bit weights in t's arrays (written by
+ * this call). d_codes: [rows, ceil(cols / 2)] bytes, column 2i in the lower
+ * half of byte i; d_scales: [rows, ceil(cols / group)] bf16; d_zeros: the same
+ * shape, u8, NULL exactly when t->d_zeros is NULL.
+ * Errors: EQ_EINVAL (NULL, an unknown type or group, rows or cols 0 or above
+ * 2^31 - 1, 2^24 tiles or more, zeros with E2M1, alignment), EQ_EHIP.
+ */
+eq_status eq_w4_pack(const eq_w4_tensor *t, const uint8_t *d_codes, const uint16_t *d_scales,
+                     const uint8_t *d_zeros, void *stream);
+
+/*
+ * eq_w4_matvec -- for every tensor i: y_i[t, r] = sum_c W_i[r, c] * x_i[t, c]
+ * for all tokens t, as one kernel launch for up to EQ_MAX_BLOCK_TENSORS
+ * tensors of one kind (type, group, zeros, x and y types). Made for few
+ * tokens: up to 64 read the weights once, more are taken 64 at a time.
+ * x: host array of n_tensors matrices [tokens, cols_i], BF16, or INT8 with
+ *    INT4 weights, or E4M3 with E2M1 weights (the 8-bit forms as
+ *    eq_add_rmsnorm and eq_silu_mul write them). y: host array of n_tensors
+ *    matrices [tokens, rows_i], F32 or BF16, overlapping nothing else.
+ * Arithmetic: exact products, fp32 accumulation (int32 within a group for
+ *    INT8 x); one rounding at the end for BF16 y. A token's y depends on no
+ *    other token's x; deterministic, but not bit-reproducible against other
+ *    summation orders or token counts.
+ * Errors: EQ_EINVAL (as eq_w4_pack; a stride below the width, a missing
+ *    scale array, an unknown type, more than 64 * 65535 tokens, 2^23 or more
+ *    rows of tiles in one launch), EQ_EUNSUPPORTED (INT8 x with E2M1
+ *    weights, E4M3 x with INT4 weights), EQ_EHIP. Everything is checked
+ *    before anything is enqueued.
+ */
+eq_status eq_w4_matvec(const eq_w4_tensor *tensors, uint32_t n_tensors, const eq_matrix *x,
+                       const eq_matrix *y, uint64_t tokens, void *stream);
 
 /* Static text for a status code. */
 const char *eq_status_string(eq_status s);

@@ -1,0 +1,32 @@
+// device_util.hpp -- small device helpers shared by the activation kernels
+// (rownorm.hip) and the 4-bit products (w4.hip). gfx950, wave64.
+#pragma once
+#include <hip/hip_runtime.h>
+
+#include <cstdint>
+
+namespace eqdev {
+
+typedef float f32x4 __attribute__((ext_vector_type(4)));
+typedef uint32_t u32x2 __attribute__((ext_vector_type(2)));
+typedef uint32_t u32x4 __attribute__((ext_vector_type(4)));
+
+// The same vectors at any element alignment: gfx950 loads and stores them
+// with the same instructions (the hardware splits what crosses a line).
+typedef u32x2 u32x2_a1 __attribute__((aligned(1)));
+typedef u32x4 u32x4_a2 __attribute__((aligned(2)));
+typedef f32x4 f32x4_a4 __attribute__((aligned(4)));
+
+typedef __bf16 bf16x2 __attribute__((ext_vector_type(2)));
+
+__device__ __forceinline__ float bf16_lo(uint32_t w) { return __uint_as_float(w << 16); }
+__device__ __forceinline__ float bf16_hi(uint32_t w) { return __uint_as_float(w & 0xFFFF0000u); }
+__device__ __forceinline__ float bf16_val(uint16_t h) { return __uint_as_float((uint32_t)h << 16); }
+
+// Two fp32 rounded to bf16 (nearest, ties to even): v_cvt_pk_bf16_f32.
+__device__ __forceinline__ uint32_t pack_bf16(float lo, float hi) {
+    const bf16x2 v = {(__bf16)lo, (__bf16)hi};
+    return __builtin_bit_cast(uint32_t, v);
+}
+
+}  // namespace eqdev

@@ -6,15 +6,18 @@ or cannot be loaded, importing this module raises.
 
 The functions keep the C names (``eq_build_tables``, ``eq_tables_from_freq``, ``eq_encode_host``,
 ``eq_parse_header``, ``eq_decode_block``, ``eq_decode_dequant_bf16``,
-``eq_decode_gemv_bf16``, ``eq_gemv_bf16``, ``eq_pipeline_*``, ``eq_bf16_from_f32``) as thin wrappers
+``eq_decode_gemv_bf16``, ``eq_gemv_bf16``, ``eq_pipeline_*``, ``eq_bf16_from_f32``, ``eq_add_rmsnorm``,
+``eq_silu_mul``, ``eq_w4_matvec``) as thin wrappers
 over numpy / torch arrays, plus a few conveniences (``build_tables``,
-``encode_host``, ``DeviceContainer``, ``decode_dequant_bf16``, ...).
+``encode_host``, ``DeviceContainer``, ``decode_dequant_bf16``, ``W4Tensor``, ...).
 """
 from __future__ import annotations
 
 import ctypes
+import functools
 import os
 import re
+import struct
 
 import numpy as np
 
@@ -31,6 +34,7 @@ EQ_MAX_BLOCK_TENSORS = 16
 EQ_CODEC_RANS = 0
 EQ_CODEC_HUFFMAN = 1
 EQ_PIPELINE_ALTERNATE, EQ_PIPELINE_OVERLAP = 0, 1
+EQ_DTYPE_INT4, EQ_DTYPE_E2M1, EQ_DTYPE_BF16, EQ_DTYPE_F32 = 3, 4, 5, 6
 
 _u32, _u64, _i32, _vp = ctypes.c_uint32, ctypes.c_uint64, ctypes.c_int32, ctypes.c_void_p
 
@@ -59,6 +63,15 @@ class eq_tensor_ref(ctypes.Structure):
     _fields_ = [("d_container", _vp), ("hdr", eq_header), ("out_offset", _u64)]
 
 
+class eq_w4_tensor(ctypes.Structure):
+    _fields_ = [("dtype", _u32), ("group", _u32), ("rows", _u64), ("cols", _u64), ("d_codes", _vp),
+                ("d_scales", _vp), ("d_zeros", _vp)]
+
+
+# eq_matrix (d, stride, d_scale, dtype, reserved), packed as bytes: a call passes several of them
+_pack_matrix = struct.Struct("@QQQII").pack
+
+
 class eq_block(ctypes.Structure):
     _fields_ = [("n_tensors", _u32), ("reserved", _u32), ("tensors", ctypes.POINTER(eq_tensor_ref)),
                 ("d_status", _vp)]
@@ -83,6 +96,10 @@ def _load():
         "eq_pipeline_run": [_vp, P(eq_block), _u32, _vp, _vp, _vp, _vp, _vp, _vp],
         "eq_pipeline_destroy": [_vp],
         "eq_bf16_from_f32": [_vp, _u64, _vp, _vp],
+        "eq_add_rmsnorm": [_vp, _vp, _vp, _vp, _u32, ctypes.c_float, _u64, _u64, _vp, _vp],
+        "eq_silu_mul": [_vp, _vp, _u64, _u64, _vp, _vp],
+        "eq_w4_pack": [P(eq_w4_tensor), _vp, _vp, _vp, _vp],
+        "eq_w4_matvec": [P(eq_w4_tensor), _u32, _vp, _vp, _u64, _vp],
         "eq_encode_device": [P(eq_tensor_desc), _vp, _vp, _vp, _vp, _u64, _vp, _u64, _vp, _u64, _vp, _vp, _vp],
         "eq_encode_device_static": [P(eq_tensor_desc), _vp, _vp, _vp, _vp, _u64, _vp, _u64, _vp, _vp, _vp],
     }
@@ -90,9 +107,11 @@ def _load():
         fn = getattr(L, name)
         fn.restype = ctypes.c_int32
         fn.argtypes = args
-    for name in ("eq_encode_device_bound", "eq_encode_device_workspace"):
+    for name in ("eq_encode_device_bound", "eq_encode_device_workspace", "eq_w4_codes_bytes", "eq_w4_groups"):
         fn = getattr(L, name)
         fn.restype = _u64
+    L.eq_w4_codes_bytes.argtypes = [_u64, _u64]
+    L.eq_w4_groups.argtypes = [_u64, _u64, _u32]
     L.eq_encode_device_bound.argtypes = [_u64, _u64, _u32, _u64]
     L.eq_encode_device_workspace.argtypes = [_u64, _u64, _u32]
     L.eq_status_string.restype = ctypes.c_char_p
@@ -309,6 +328,171 @@ def eq_gemv_bf16(w, rows: int, cols: int, x, y, stream=None, w_offset_elems: int
 def eq_bf16_from_f32(x, out, stream=None) -> None:
     _check("eq_bf16_from_f32", _lib.eq_bf16_from_f32(x.data_ptr(), x.numel(), out.data_ptr(),
                                                      _stream_handle(stream)))
+
+
+# ---------------------------------------------------------------------------
+# The steps around the weight products (torch tensors on the GPU)
+# ---------------------------------------------------------------------------
+@functools.lru_cache(maxsize=None)
+def _activation_types() -> dict:
+    torch = _torch()
+    return {torch.float32: EQ_DTYPE_F32, torch.bfloat16: EQ_DTYPE_BF16, torch.int8: EQ_DTYPE_INT8,
+            torch.float8_e4m3fn: EQ_DTYPE_E4M3}
+
+
+@functools.lru_cache(maxsize=None)
+def _raw_stream():
+    """The current stream's handle by device index (torch.cuda.current_stream
+    builds an object for it, which costs more than a small kernel's launch)."""
+    torch = _torch()
+    return getattr(torch._C, "_cuda_getCurrentRawStream", None) or (
+        lambda index: torch.cuda.current_stream(index).cuda_stream)
+
+
+def _stream_of(stream, t) -> int | None:
+    return _raw_stream()(t.get_device()) if stream is None else _stream_handle(stream)
+
+
+def _matrix(name: str, t, tokens: int, cols: int, scale=None) -> bytes:
+    """eq_matrix of a [tokens, cols] tensor (or [cols] for one token) whose last
+    dimension is dense."""
+    shape, stride = t.shape, t.stride()
+    if len(shape) == 2:
+        rows, ld = shape[0], stride[0]
+    elif len(shape) == 1:
+        rows, ld = 1, shape[0]
+    else:
+        raise ValueError(f"{name}: one or two dimensions, got shape {tuple(shape)}")
+    if rows != tokens or shape[-1] != cols:
+        raise ValueError(f"{name}: expected [{tokens}, {cols}], got {tuple(shape)}")
+    if stride[-1] != 1 and cols > 1:
+        raise ValueError(f"{name}: elements of a row must be contiguous")
+    if rows <= 1 or cols == 1 and ld < 1:
+        ld = max(ld, cols)
+    dtype = _activation_types().get(t.dtype)
+    if dtype is None:
+        raise ValueError(f"{name}: type {t.dtype} is not supported")
+    d_scale = 0
+    if dtype == EQ_DTYPE_INT8 or dtype == EQ_DTYPE_E4M3:
+        if scale is None:
+            raise ValueError(f"{name}: an 8-bit matrix needs its scales (fp32, one per row)")
+        if scale.dtype != _torch().float32 or scale.numel() != tokens or not scale.is_contiguous():
+            raise ValueError(f"{name}: scales must be {tokens} contiguous fp32 values")
+        if not scale.is_cuda:
+            raise ValueError(f"{name}: scales must be on the GPU")
+        d_scale = scale.data_ptr()
+    elif scale is not None:
+        raise ValueError(f"{name}: scales belong to 8-bit types")
+    if not t.is_cuda:
+        raise ValueError(f"{name}: must be on the GPU")
+    return _pack_matrix(t.data_ptr(), ld, d_scale, dtype, 0)
+
+
+def _size(t) -> tuple[int, int]:
+    shape = t.shape
+    return (shape[0], shape[1]) if len(shape) == 2 else (1, shape[0]) if len(shape) == 1 else (0, 0)
+
+
+def eq_add_rmsnorm(x, weight, eps: float, out, out_scale=None, residual=None, residual_out=None, stream=None) -> None:
+    """out = norm(x + residual) * weight per row of x ([tokens, cols] or [cols];
+    fp32 or bf16); the sum, rounded to residual's type, goes to residual_out
+    (default: into residual itself). out: bfloat16, or int8 / float8_e4m3fn
+    with out_scale (fp32, one per token). weight: bf16 or fp32 [cols], or None."""
+    tokens, cols = _size(x)
+    r = ro = w = None
+    w_type = 0
+    if residual is not None:
+        r = _matrix("residual", residual, tokens, cols)
+        ro = r if residual_out is None else _matrix("residual_out", residual_out, tokens, cols)
+    elif residual_out is not None:
+        raise ValueError("residual_out without a residual")
+    if weight is not None:
+        w_type = _activation_types().get(weight.dtype, 0)
+        if weight.numel() != cols or not weight.is_contiguous() or not weight.is_cuda:
+            raise ValueError(f"weight: {cols} contiguous values on the GPU")
+        w = weight.data_ptr()
+    _check("eq_add_rmsnorm", _lib.eq_add_rmsnorm(
+        _matrix("x", x, tokens, cols), r, ro, w, w_type, eps, tokens, cols,
+        _matrix("out", out, tokens, cols, out_scale), _stream_of(stream, x)))
+
+
+def eq_silu_mul(gate, up, out, out_scale=None, stream=None) -> None:
+    """out = silu(gate) * up per element ([tokens, cols] or [cols]; fp32 or
+    bf16, rows may be strided: two halves of one buffer). out and out_scale as
+    for eq_add_rmsnorm."""
+    tokens, cols = _size(gate)
+    _check("eq_silu_mul", _lib.eq_silu_mul(
+        _matrix("gate", gate, tokens, cols), _matrix("up", up, tokens, cols), tokens, cols,
+        _matrix("out", out, tokens, cols, out_scale), _stream_of(stream, gate)))
+
+
+class W4Tensor:
+    """A 4-bit weight matrix in the kernels' layout (eq_w4_pack), on the device
+    of `codes`: uint8 [rows, ceil(cols / 2)], column 2i in the lower half of
+    byte i; scales bfloat16 and zeros uint8 (INT4, optional)
+    [rows, ceil(cols / group)]. The arrays are written on the current stream;
+    order other streams after it."""
+
+    def __init__(self, codes, scales, zeros=None, dtype: int = EQ_DTYPE_INT4, group: int = 128,
+                 cols: int | None = None):
+        torch = _torch()
+        if codes.dtype != torch.uint8 or codes.dim() != 2 or not codes.is_contiguous() or not codes.is_cuda:
+            raise ValueError("codes: a contiguous uint8 [rows, ceil(cols / 2)] tensor on the GPU")
+        rows = codes.shape[0]
+        cols = 2 * codes.shape[1] if cols is None else cols
+        if -(-cols // 2) != codes.shape[1]:
+            raise ValueError(f"codes: {codes.shape[1]} bytes per row do not hold {cols} columns")
+        n = int(_lib.eq_w4_groups(rows, cols, group))
+        if n == 0:
+            raise EqError("eq_w4_pack", EQ_EINVAL)
+        shape = (rows, -(-cols // group))
+        if scales.dtype != torch.bfloat16 or tuple(scales.shape) != shape or not scales.is_contiguous() \
+                or scales.device != codes.device:
+            raise ValueError(f"scales: a contiguous bfloat16 {shape} tensor beside the codes")
+        if zeros is not None and (zeros.dtype != torch.uint8 or tuple(zeros.shape) != shape
+                                  or not zeros.is_contiguous() or zeros.device != codes.device):
+            raise ValueError(f"zeros: a contiguous uint8 {shape} tensor beside the codes")
+        self.dtype, self.group, self.rows, self.cols = dtype, group, rows, cols
+        dev = codes.device
+        self.codes = torch.empty(int(_lib.eq_w4_codes_bytes(rows, cols)), dtype=torch.uint8, device=dev)
+        self.scales = torch.empty(n, dtype=torch.bfloat16, device=dev)
+        self.zeros = torch.empty(n, dtype=torch.uint8, device=dev) if zeros is not None else None
+        self.c = eq_w4_tensor(dtype=dtype, group=group, rows=rows, cols=cols, d_codes=self.codes.data_ptr(),
+                              d_scales=self.scales.data_ptr(),
+                              d_zeros=self.zeros.data_ptr() if zeros is not None else None)
+        _check("eq_w4_pack", _lib.eq_w4_pack(
+            ctypes.byref(self.c), codes.data_ptr(), scales.data_ptr(),
+            zeros.data_ptr() if zeros is not None else None, _stream_of(None, codes)))
+
+    @property
+    def nbytes(self) -> int:
+        return self.codes.numel() + 2 * self.scales.numel() + (self.zeros.numel() if self.zeros is not None else 0)
+
+
+class W4Block:
+    """Tensors multiplied by one call (eq_w4_matvec). Keeps them alive."""
+
+    def __init__(self, tensors):
+        self.tensors = list(tensors)
+        self.c = (eq_w4_tensor * max(1, len(self.tensors)))(*[t.c for t in self.tensors])
+
+
+def eq_w4_matvec(block: W4Block, xs, ys, x_scales=None, stream=None) -> None:
+    """ys[i] = xs[i] @ W_i.T for every tensor of the block: xs[i]
+    [tokens, cols_i] bfloat16, or int8 (INT4 weights) / float8_e4m3fn (E2M1
+    weights) with x_scales[i] (fp32, one per token); ys[i] [tokens, rows_i]
+    fp32 or bfloat16. One dimension means one token."""
+    tensors = block.tensors
+    n = len(tensors)
+    if len(xs) != n or len(ys) != n or x_scales is not None and len(x_scales) != n:
+        raise ValueError("one x, one y and, with scales, one x_scales entry per tensor")
+    if n == 0:
+        return
+    tokens = _size(xs[0])[0]
+    xm = b"".join([_matrix("x", x, tokens, t.cols, x_scales[i] if x_scales is not None else None)
+                   for i, (t, x) in enumerate(zip(tensors, xs))])
+    ym = b"".join([_matrix("y", y, tokens, t.rows) for t, y in zip(tensors, ys)])
+    _check("eq_w4_matvec", _lib.eq_w4_matvec(block.c, n, xm, ym, tokens, _stream_of(stream, xs[0])))
 
 
 class Pipeline:
