@@ -241,7 +241,8 @@ def test_pack_layout():
         zs = t.zeros.cpu().numpy().reshape(scales.shape) if zeros else None
         for r in range(16 * -(-rows // 16)):
             for c in range(128 * k_tiles):
-                word = int(words[r // 16, c // 128, c % 32 // 8, r % 16, c % 128 // 32])
+                quarter, within = c % group // (group // 4), c % group % (group // 4)
+                word = int(words[r // 16, c // 128, quarter, r % 16, (c % 128 // group * (group // 4) + within) // 8])
                 got = word >> 4 * place.index(c % 8) & 15
                 assert got == (int(w.codes[r, c]) if r < rows and c < cols else 0)
             for g in range(k_tiles * per):
