@@ -452,12 +452,11 @@ eq_status eq_silu_mul(const eq_matrix *gate, const eq_matrix *up, uint64_t token
  * eq_w4_pack lays out once, when a model is loaded (row-major codes were read
  * at 4.2-5.0 TB/s against 6.1-6.4 for tiles): tile (r / 16, c / 128) is 1 KiB
  * at (r / 16 * ceil(cols / 128) + c / 128) * 1024, the 16 bytes of its row
- * i and quarter k at (16 * k + i) * 16: four u32, together holding
- * group / 4 consecutive columns of each group of the tile, from column
- * k * (group / 4) of the group on, 8 to a word, 4 bits each from bit 0 up: for
- * E2M1 in the order 0 1 2 3 4 5 6 7, for INT4 0 2 4 6 1 3 5 7. Scales and zeros
- * go the same way: entry (tile * 16 + i) * (128 / group) + group within the
- * tile.
+ * i and quarter k at (16 * k + i) * 16: four u32. Word j holds the 8 columns
+ * from 64 * (j / 2) + 16 * k + 8 * (j % 2) on (group 32: from 32 * j + 8 * k
+ * on), 4 bits each from bit 0 up, for E2M1 in the order 0 1 2 3 4 5 6 7, for
+ * INT4 0 2 4 6 1 3 5 7. Scales and zeros go the same way: entry
+ * (tile * 16 + i) * (128 / group) + group within the tile.
  * Padding holds zeros.
  */
 typedef struct eq_w4_tensor {

@@ -25,6 +25,7 @@
 #include <hip/hip_runtime.h>
 
 #include <cstdint>
+#include <type_traits>
 
 #include "../../include/eq.h"
 #include "device_util.hpp"
@@ -49,78 +50,33 @@ struct W4Args {
     void *y;
     uint64_t ldx, ldy;
     uint32_t rows, cols;
-    uint32_t wg_begin;  // first workgroup of this tensor
-    uint32_t k_waves;   // waves that share out the columns of one row of tiles (1, 2, 4, 8)
+    uint32_t k_tiles, row_tiles;  // columns and rows of tiles
+    uint32_t kw_log2;             // 1 << kw_log2 waves share out the columns (k_w4)
     uint32_t group;
 };
 
 struct W4Launch {
-    W4Args t[EQ_MAX_BLOCK_TENSORS];
-    uint32_t n_tensors;
+    uint32_t wg_begin[EQ_MAX_BLOCK_TENSORS];  // first workgroup of each tensor, 2^32 - 1 past the last
     uint32_t tokens;
     uint32_t y_f32;
+    W4Args t[EQ_MAX_BLOCK_TENSORS];
 };
 
-// Column within a tile of the first of the 8 weights in word j of a lane:
-// of every group (of `span` columns) a quarter wave holds span / 4
-// consecutive ones, so that a lane's activations are as contiguous as the
-// groups allow.
-__host__ __device__ constexpr uint32_t word_col(uint32_t span, uint32_t quarter, uint32_t j) {
-    const uint32_t words = span / 32;  // words of a lane per group
-    return j / words * span + quarter * (span / 4) + j % words * 8;
+// The tensor of a workgroup. (One load of all the starts: walking them took a
+// dependent load per tensor.)
+__device__ __forceinline__ uint32_t tensor_of(const W4Launch &a, uint32_t wg) {
+    uint32_t ti = 0;
+#pragma unroll
+    for (uint32_t i = 1; i < EQ_MAX_BLOCK_TENSORS; ++i) ti += wg >= a.wg_begin[i];
+    return ti;
 }
 
-// Activations of one lane for a tile: word j's 8 values at w[j * N].
-template <uint32_t X>
-struct XFrag {
-    static constexpr uint32_t N = X == EQ_DTYPE_BF16 ? 4 : 2;
-    uint32_t w[4 * N];
-};
-
-// `row` points at the tile's first column. left: columns that exist from
-// there on (FULL: at least 128).
-template <uint32_t X, uint32_t S, bool FULL>
-__device__ __forceinline__ XFrag<X> load_x(const void *row, uint32_t quarter, uint32_t left) {
-    XFrag<X> f;
-    if constexpr (X == EQ_DTYPE_BF16) {
-        const uint16_t *p = static_cast<const uint16_t *>(row);
-#pragma unroll
-        for (uint32_t j = 0; j < 4; ++j) {
-            const uint32_t at = word_col(S, quarter, j);
-            u32x4 v = {0, 0, 0, 0};
-            if (FULL || at + 8 <= left) {
-                v = *reinterpret_cast<const u32x4_a2 *>(p + at);
-            } else {
-                for (uint32_t i = 0; i < 8; ++i)
-                    if (at + i < left) v[i / 2] |= (uint32_t)p[at + i] << (16 * (i & 1));
-            }
-            for (int i = 0; i < 4; ++i) f.w[4 * j + i] = v[i];
-        }
-    } else {
-        const uint8_t *p = static_cast<const uint8_t *>(row);
-        if constexpr (FULL && S >= 64) {
-#pragma unroll
-            for (uint32_t j = 0; j < 4; j += 2) {
-                const u32x4 v = *reinterpret_cast<const u32x4_a1 *>(p + word_col(S, quarter, j));
-                for (int i = 0; i < 4; ++i) f.w[2 * j + i] = v[i];
-            }
-        } else {
-#pragma unroll
-            for (uint32_t j = 0; j < 4; ++j) {
-                const uint32_t at = word_col(S, quarter, j);
-                u32x2 v = {0, 0};
-                if (FULL || at + 8 <= left) {
-                    v = *reinterpret_cast<const u32x2_a1 *>(p + at);
-                } else {
-                    for (uint32_t i = 0; i < 8; ++i)
-                        if (at + i < left) v[i / 4] |= (uint32_t)p[at + i] << (8 * (i & 3));
-                }
-                f.w[2 * j] = v[0];
-                f.w[2 * j + 1] = v[1];
-            }
-        }
-    }
-    return f;
+// Column within a tile of the first of the 8 weights in word j of a lane:
+// word pairs hold 16 consecutive columns of a block of 64 (one 16-byte load of
+// 8-bit activations), so that no matrix instruction mixes groups of 64; with
+// groups of 32, words hold 8 of a block of 32.
+__host__ __device__ constexpr uint32_t word_col(uint32_t group, uint32_t quarter, uint32_t j) {
+    return group == 32 ? j * 32 + quarter * 8 : j / 2 * 64 + quarter * 16 + j % 2 * 8;
 }
 
 // One word of codes (8 weights of one row) as bf16.
@@ -128,11 +84,13 @@ template <uint32_t W, bool Z>
 __device__ __forceinline__ u32x4 decode8(uint32_t w) {
     u32x4 r;
     if constexpr (W == EQ_DTYPE_INT4) {
+        constexpr uint32_t mask = 0x00780078u;
         constexpr uint32_t bias = Z ? 0x41804180u : 0x41C041C0u;  // signed codes: the sign bit is flipped
-        r[0] = ((w << 3) & 0x00780078u) ^ bias;
-        r[1] = ((w >> 1) & 0x00780078u) ^ bias;
-        r[2] = ((w >> 5) & 0x00780078u) ^ bias;
-        r[3] = ((w >> 9) & 0x00780078u) ^ bias;
+        constexpr int kAndXor = (0xF0 & 0xCC) ^ 0xAA;             // (a & b) ^ c
+        r[0] = __builtin_amdgcn_bitop3_b32(w << 3, mask, bias, kAndXor);
+        r[1] = __builtin_amdgcn_bitop3_b32(w >> 1, mask, bias, kAndXor);
+        r[2] = __builtin_amdgcn_bitop3_b32(w >> 5, mask, bias, kAndXor);
+        r[3] = __builtin_amdgcn_bitop3_b32(w >> 9, mask, bias, kAndXor);
     } else {
         r[0] = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(w, 1.0f, 0));
         r[1] = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(w, 1.0f, 1));
@@ -142,219 +100,329 @@ __device__ __forceinline__ u32x4 decode8(uint32_t w) {
     return r;
 }
 
-__device__ __forceinline__ f32x4 mfma_bf16(u32x4 a, u32x4 b, f32x4 c) {
-    return __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf16x8, a), __builtin_bit_cast(bf16x8, b), c, 0,
-                                                   0, 0);
-}
-__device__ __forceinline__ i32x4 mfma_i8x64(u32x4 a, u32x4 b, i32x4 c) {
-    return __builtin_amdgcn_mfma_i32_16x16x64_i8(__builtin_bit_cast(i32x4, a), __builtin_bit_cast(i32x4, b), c, 0, 0, 0);
-}
-__device__ __forceinline__ i32x4 mfma_i8x32(u32x2 a, u32x2 b, i32x4 c) {
-    return __builtin_amdgcn_mfma_i32_16x16x32_i8(__builtin_bit_cast(long, a), __builtin_bit_cast(long, b), c, 0, 0, 0);
+// 8 E4M3 values as bf16 (exact).
+__device__ __forceinline__ u32x4 widen_e4m3(u32x2 v) {
+    u32x4 o;
+    for (int i = 0; i < 4; ++i)
+        o[i] = __builtin_bit_cast(uint32_t, i & 1 ? __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(v[i / 2], 1.0f, true)
+                                                  : __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(v[i / 2], 1.0f, false));
+    return o;
 }
 
-// What a wave reads of one column of tiles: R rows of tiles, NT token tiles.
-template <uint32_t X, uint32_t S, bool Z, int NT, int R>
-struct Stage {
-    u32x4 c[R];
-    uint32_t s[R][2];  // bf16 scales of the lane's row: 128 / S of them
-    uint32_t z[R];     // zeros, a byte each
-    XFrag<X> x[NT];
+// A kind of weight and activation: a lane's codes of a tile are Q pieces, one
+// per matrix instruction; a group is PG pieces.
+//   Raw: a lane's activations of a piece as loaded; Op: a matrix operand.
+template <uint32_t W, uint32_t X, uint32_t S, bool Z>
+struct Kind {  // bf16 products
+    static constexpr uint32_t Q = 4, PG = S / 32;
+    static constexpr bool kSumX = W == EQ_DTYPE_INT4;  // sum(x) is needed
+    static constexpr float kScale = 1.0f;
+    typedef typename std::conditional<X == EQ_DTYPE_BF16, u32x4, u32x2>::type Raw;
+    typedef u32x4 Op;
+    typedef f32x4 Sum;
+    static __device__ __forceinline__ uint32_t col(uint32_t quarter, uint32_t p) { return word_col(S, quarter, p); }
+    static __device__ __forceinline__ Op acts(Raw r) {
+        if constexpr (X == EQ_DTYPE_BF16) {
+            return r;
+        } else {
+            return widen_e4m3(r);
+        }
+    }
+    static __device__ __forceinline__ Op codes(u32x4 c, uint32_t p) { return decode8<W, Z>(c[p]); }
+    static __device__ __forceinline__ Op ones() { return Op{0x3F803F80u, 0x3F803F80u, 0x3F803F80u, 0x3F803F80u}; }
+    static __device__ __forceinline__ Sum mma(Op a, Op b, Sum c) {
+        return __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf16x8, a), __builtin_bit_cast(bf16x8, b), c, 0,
+                                                       0, 0);
+    }
+    static __device__ __forceinline__ float value(float d, float sum_x, float zero) {
+        return kSumX ? fmaf(-(Z ? 16.0f + zero : 24.0f), sum_x, d) : d;
+    }
 };
 
-template <uint32_t X, uint32_t S, bool Z, int NT, int R, bool FULL>
-__device__ __forceinline__ void load_stage(Stage<X, S, Z, NT, R> &st, const W4Args &T, const u32x4 *codes,
-                                           const uint16_t *scales, const uint8_t *zeros, const char *const *x_row,
-                                           uint32_t kt, uint32_t k_tiles, uint32_t quarter) {
-    constexpr uint32_t P = kTileCols / S;
-#pragma unroll
-    for (int r = 0; r < R; ++r) {
-        const uint64_t tile = (uint64_t)r * k_tiles + kt;
-        st.c[r] = __builtin_nontemporal_load(codes + tile * 64);
-        const uint16_t *sp = scales + tile * 16 * P;
-        if constexpr (P == 1) st.s[r][0] = *sp;
-        else if constexpr (P == 2) st.s[r][0] = *reinterpret_cast<const uint32_t *>(sp);
-        else {
-            const u32x2 v = *reinterpret_cast<const u32x2 *>(sp);
-            st.s[r][0] = v[0];
-            st.s[r][1] = v[1];
-        }
-        if constexpr (Z) {
-            const uint8_t *zp = zeros + tile * 16 * P;
-            if constexpr (P == 1) st.z[r] = *zp;
-            else if constexpr (P == 2) st.z[r] = *reinterpret_cast<const uint16_t *>(zp);
-            else st.z[r] = *reinterpret_cast<const uint32_t *>(zp);
-        }
+template <uint32_t W, uint32_t S, bool Z>
+struct KindE4M3x64 {  // E4M3 in groups of 64 or 128: 64 columns a piece, two instructions
+    typedef Kind<W, EQ_DTYPE_BF16, S, Z> B;
+    static constexpr uint32_t Q = 2, PG = S / 64;
+    static constexpr bool kSumX = false;
+    static constexpr float kScale = 1.0f;
+    typedef u32x4 Raw;
+    struct Op { u32x4 h[2]; };
+    typedef f32x4 Sum;
+    static __device__ __forceinline__ uint32_t col(uint32_t quarter, uint32_t p) { return word_col(S, quarter, 2 * p); }
+    static __device__ __forceinline__ Op acts(Raw r) {
+        return Op{{widen_e4m3(u32x2{r[0], r[1]}), widen_e4m3(u32x2{r[2], r[3]})}};
     }
-    constexpr size_t XB = X == EQ_DTYPE_BF16 ? 2 : 1;
-#pragma unroll
-    for (int n = 0; n < NT; ++n)
-        st.x[n] = load_x<X, S, FULL>(x_row[n] + (uint64_t)kt * kTileCols * XB, quarter, T.cols - kt * kTileCols);
+    static __device__ __forceinline__ Op codes(u32x4 c, uint32_t p) { return Op{{B::codes(c, 2 * p), B::codes(c, 2 * p + 1)}}; }
+    static __device__ __forceinline__ Op ones() { return Op{}; }
+    static __device__ __forceinline__ Sum mma(Op a, Op b, Sum c) { return B::mma(a.h[1], b.h[1], B::mma(a.h[0], b.h[0], c)); }
+    static __device__ __forceinline__ float value(float d, float, float) { return d; }
+};
+template <>
+struct Kind<EQ_DTYPE_E2M1, EQ_DTYPE_E4M3, 64, false> : KindE4M3x64<EQ_DTYPE_E2M1, 64, false> {};
+template <>
+struct Kind<EQ_DTYPE_E2M1, EQ_DTYPE_E4M3, 128, false> : KindE4M3x64<EQ_DTYPE_E2M1, 128, false> {};
+
+// int8 products. The bytes of a word's lower halves are columns 0 4 1 5 of its
+// eight, those of its upper halves 2 6 3 7; activations are put in that order.
+__device__ __forceinline__ u32x2 int8_order(uint32_t lo, uint32_t hi) {
+    return u32x2{__builtin_amdgcn_perm(hi, lo, 0x05010400u), __builtin_amdgcn_perm(hi, lo, 0x07030602u)};
+}
+template <bool Z>
+__device__ __forceinline__ u32x2 int8_codes(uint32_t w) {
+    if (Z) return u32x2{w & 0x0F0F0F0Fu, (w >> 4) & 0x0F0F0F0Fu};
+    return u32x2{(w << 4) & 0xF0F0F0F0u, w & 0xF0F0F0F0u};  // 16 q
+}
+template <bool Z>
+__device__ __forceinline__ float int8_value(int32_t d, int32_t sum_x, float zero) {
+    // |d| and |zero * sum_x| stay below 2^24: exact
+    return Z ? fmaf(-zero, (float)sum_x, (float)d) : (float)d;
 }
 
-// acc += the stage's products.
-template <uint32_t W, uint32_t X, uint32_t S, bool Z, int NT, int R>
-__device__ __forceinline__ void compute(const Stage<X, S, Z, NT, R> &st, f32x4 (&acc)[NT][R]) {
-    constexpr uint32_t P = kTileCols / S, J = 4 / P;  // groups of a tile, words of a lane per group
-    auto scale = [&](int r, uint32_t g) {
-        const uint32_t w = st.s[r][g / 2];
-        return g & 1 ? bf16_hi(w) : bf16_lo(w);
-    };
-    auto zero = [&](int r, uint32_t g) { return (float)(st.z[r] >> (8 * g) & 255u); };
-    if constexpr (X == EQ_DTYPE_INT8) {
-#pragma unroll
-        for (uint32_t g = 0; g < P; ++g) {
-            u32x4 a[NT][(J + 1) / 2];  // a group's activations in the order of the code bytes (J = 1: half used)
-            i32x4 sx[NT] = {};
-#pragma unroll
-            for (int n = 0; n < NT; ++n) {
-                for (uint32_t j = 0; j < J; ++j) {
-                    const uint32_t lo = st.x[n].w[2 * (g * J + j)], hi = st.x[n].w[2 * (g * J + j) + 1];
-                    a[n][j / 2][2 * (j & 1)] = __builtin_amdgcn_perm(hi, lo, 0x05010400u);      // columns 0 4 1 5
-                    a[n][j / 2][2 * (j & 1) + 1] = __builtin_amdgcn_perm(hi, lo, 0x07030602u);  // columns 2 6 3 7
-                }
-                if constexpr (Z) {
-                    constexpr uint32_t one = 0x01010101u;
-                    if constexpr (J == 1) sx[n] = mfma_i8x32(u32x2{a[n][0][0], a[n][0][1]}, u32x2{one, one}, sx[n]);
-                    else
-                        for (uint32_t m = 0; m < J / 2; ++m) sx[n] = mfma_i8x64(a[n][m], u32x4{one, one, one, one}, sx[n]);
-                }
-            }
-#pragma unroll
-            for (int r = 0; r < R; ++r) {
-                uint32_t b[2 * J];
-                for (uint32_t j = 0; j < J; ++j) {
-                    const uint32_t w = st.c[r][g * J + j];
-                    b[2 * j] = Z ? w & 0x0F0F0F0Fu : (w << 4) & 0xF0F0F0F0u;
-                    b[2 * j + 1] = Z ? (w >> 4) & 0x0F0F0F0Fu : w & 0xF0F0F0F0u;
-                }
-                const float s = Z ? scale(r, g) : scale(r, g) * 0.0625f;
-#pragma unroll
-                for (int n = 0; n < NT; ++n) {
-                    i32x4 d = {};
-                    if constexpr (J == 1) d = mfma_i8x32(u32x2{a[n][0][0], a[n][0][1]}, u32x2{b[0], b[1]}, d);
-                    else
-                        for (uint32_t m = 0; m < J / 2; ++m)
-                            d = mfma_i8x64(a[n][m], u32x4{b[4 * m], b[4 * m + 1], b[4 * m + 2], b[4 * m + 3]}, d);
-                    for (int i = 0; i < 4; ++i) {
-                        float v = (float)d[i];  // below 2^24: exact, as is the zeros' part
-                        if constexpr (Z) v = fmaf(-zero(r, g), (float)sx[n][i], v);
-                        acc[n][r][i] = fmaf(s, v, acc[n][r][i]);
-                    }
-                }
-            }
+template <uint32_t S, bool Z>
+struct Kind<EQ_DTYPE_INT4, EQ_DTYPE_INT8, S, Z> {  // 64 columns an instruction
+    static constexpr uint32_t Q = 2, PG = S / 64;
+    static constexpr bool kSumX = Z;
+    static constexpr float kScale = Z ? 1.0f : 0.0625f;
+    typedef u32x4 Raw;
+    typedef u32x4 Op;
+    typedef i32x4 Sum;
+    static __device__ __forceinline__ uint32_t col(uint32_t quarter, uint32_t p) { return word_col(S, quarter, 2 * p); }
+    static __device__ __forceinline__ Op acts(Raw r) {
+        const u32x2 a = int8_order(r[0], r[1]), b = int8_order(r[2], r[3]);
+        return Op{a[0], a[1], b[0], b[1]};
+    }
+    static __device__ __forceinline__ Op codes(u32x4 c, uint32_t p) {
+        const u32x2 a = int8_codes<Z>(c[2 * p]), b = int8_codes<Z>(c[2 * p + 1]);
+        return Op{a[0], a[1], b[0], b[1]};
+    }
+    static __device__ __forceinline__ Op ones() { return Op{0x01010101u, 0x01010101u, 0x01010101u, 0x01010101u}; }
+    static __device__ __forceinline__ Sum mma(Op a, Op b, Sum c) {
+        return __builtin_amdgcn_mfma_i32_16x16x64_i8(__builtin_bit_cast(i32x4, a), __builtin_bit_cast(i32x4, b), c, 0, 0,
+                                                     0);
+    }
+    static __device__ __forceinline__ float value(int32_t d, int32_t sum_x, float zero) { return int8_value<Z>(d, sum_x, zero); }
+};
+
+template <bool Z>
+struct Kind<EQ_DTYPE_INT4, EQ_DTYPE_INT8, 32, Z> {  // groups of 32: 32 columns an instruction
+    static constexpr uint32_t Q = 4, PG = 1;
+    static constexpr bool kSumX = Z;
+    static constexpr float kScale = Z ? 1.0f : 0.0625f;
+    typedef u32x2 Raw;
+    typedef u32x2 Op;
+    typedef i32x4 Sum;
+    static __device__ __forceinline__ uint32_t col(uint32_t quarter, uint32_t p) { return word_col(32, quarter, p); }
+    static __device__ __forceinline__ Op acts(Raw r) { return int8_order(r[0], r[1]); }
+    static __device__ __forceinline__ Op codes(u32x4 c, uint32_t p) { return int8_codes<Z>(c[p]); }
+    static __device__ __forceinline__ Op ones() { return Op{0x01010101u, 0x01010101u}; }
+    static __device__ __forceinline__ Sum mma(Op a, Op b, Sum c) {
+        return __builtin_amdgcn_mfma_i32_16x16x32_i8(__builtin_bit_cast(long, a), __builtin_bit_cast(long, b), c, 0, 0, 0);
+    }
+    static __device__ __forceinline__ float value(int32_t d, int32_t sum_x, float zero) { return int8_value<Z>(d, sum_x, zero); }
+};
+
+// Activations at p, of which `left` elements of X exist (FULL: all of them);
+// the rest reads as zero.
+template <uint32_t X, typename Raw, bool FULL>
+__device__ __forceinline__ Raw load_raw(const char *p, int32_t left) {
+    constexpr int32_t XB = X == EQ_DTYPE_BF16 ? 2 : 1, N = sizeof(Raw) / XB;
+    if (FULL || left >= N) {
+        if constexpr (XB == 2) return *reinterpret_cast<const u32x4_a2 *>(p);
+        else if constexpr (sizeof(Raw) == 16) return *reinterpret_cast<const u32x4_a1 *>(p);
+        else return *reinterpret_cast<const u32x2_a1 *>(p);
+    }
+    Raw r = {};
+    for (int32_t i = 0; i < N; ++i)
+        if (i < left) {
+            const uint32_t v = XB == 2 ? reinterpret_cast<const uint16_t *>(p)[i] : reinterpret_cast<const uint8_t *>(p)[i];
+            r[i * XB / 4] |= v << (8 * (i * XB % 4));
         }
-    } else {
-        const u32x4 ones = {0x3F803F80u, 0x3F803F80u, 0x3F803F80u, 0x3F803F80u};
+    return r;
+}
+
+// What a wave reads of the weights of one column of tiles: R rows of tiles.
+template <uint32_t S, bool Z, int R>
+struct Weights {
+    static constexpr uint32_t P = kTileCols / S;  // groups of a tile
+    u32x4 c[R];
+    uint32_t s[R][2];  // bf16 scales of the lane's row, one per group of the tile
+    uint32_t z[R];     // zeros, a byte each
+
+    // tile0: the first of the wave's rows of tiles, lane offsets apart from it
+    // (a uniform base in scalar registers and one 32-bit offset per lane)
+    __device__ __forceinline__ void load(const W4Args &T, uint64_t tile0, uint32_t kt, uint32_t k_tiles, uint32_t lane) {
 #pragma unroll
-        for (uint32_t g = 0; g < P; ++g) {
-            f32x4 d[NT][R] = {}, sx[NT] = {};
-#pragma unroll
-            for (uint32_t j = g * J; j < (g + 1) * J; ++j) {
-                u32x4 xa[NT];
-#pragma unroll
-                for (int n = 0; n < NT; ++n) {
-                    if constexpr (X == EQ_DTYPE_BF16) {
-                        for (int i = 0; i < 4; ++i) xa[n][i] = st.x[n].w[4 * j + i];
-                    } else {
-                        for (int i = 0; i < 4; ++i) {
-                            const uint32_t v = st.x[n].w[2 * j + i / 2];
-                            xa[n][i] = __builtin_bit_cast(
-                                uint32_t, i & 1 ? __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(v, 1.0f, true)
-                                                : __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(v, 1.0f, false));
-                        }
-                    }
-                    if constexpr (W == EQ_DTYPE_INT4) sx[n] = mfma_bf16(xa[n], ones, sx[n]);
-                }
-#pragma unroll
-                for (int r = 0; r < R; ++r) {
-                    const u32x4 b = decode8<W, Z>(st.c[r][j]);
-#pragma unroll
-                    for (int n = 0; n < NT; ++n) d[n][r] = mfma_bf16(xa[n], b, d[n][r]);
-                }
+        for (int r = 0; r < R; ++r) {
+            const uint64_t tile = tile0 + (uint64_t)r * k_tiles + kt;
+            c[r] = __builtin_nontemporal_load(T.codes + tile * 64 + lane);  // read once: plain loads took 8% longer
+            const uint16_t *sp = T.scales + tile * 16 * P + (lane & 15u) * P;
+            if constexpr (P == 1) s[r][0] = *sp;
+            else if constexpr (P == 2) s[r][0] = *reinterpret_cast<const uint32_t *>(sp);
+            else {
+                const u32x2 v = *reinterpret_cast<const u32x2 *>(sp);
+                s[r][0] = v[0];
+                s[r][1] = v[1];
             }
-#pragma unroll
-            for (int r = 0; r < R; ++r) {
-                const float s = scale(r, g);
-                float off = 24.0f;  // 16 + 8
-                if constexpr (Z) off = 16.0f + zero(r, g);
-                for (int n = 0; n < NT; ++n)
-                    for (int i = 0; i < 4; ++i) {
-                        const float v = W == EQ_DTYPE_INT4 ? fmaf(-off, sx[n][i], d[n][r][i]) : d[n][r][i];
-                        acc[n][r][i] = fmaf(s, v, acc[n][r][i]);
-                    }
+            if constexpr (Z) {
+                const uint8_t *zp = T.zeros + tile * 16 * P + (lane & 15u) * P;
+                if constexpr (P == 1) z[r] = *zp;
+                else if constexpr (P == 2) z[r] = *reinterpret_cast<const uint16_t *>(zp);
+                else z[r] = *reinterpret_cast<const uint32_t *>(zp);
             }
         }
     }
+    __device__ __forceinline__ float scale(int r, uint32_t g) const {
+        const uint32_t w = P == 4 ? (g & 2 ? s[r][1] : s[r][0]) : s[r][0];
+        return P == 1 || !(g & 1) ? bf16_lo(w) : bf16_hi(w);
+    }
+    __device__ __forceinline__ float zero(int r, uint32_t g) const {
+        return Z ? (float)(P == 1 ? z[r] : z[r] >> (8 * g) & 255u) : 0.0f;
+    }
+};
+
+__device__ __forceinline__ void store_y(const W4Args &T, bool f32, uint32_t t, uint32_t row, float v) {
+    if (f32) static_cast<float *>(T.y)[t * T.ldy + row] = v;
+    else static_cast<uint16_t *>(T.y)[t * T.ldy + row] = (uint16_t)pack_bf16(v, 0.0f);
 }
 
 // A workgroup's 8 waves are (8 / k_waves) x k_waves: wave (rw, kw) owns R rows
-// of tiles and every k_waves-th column of tiles, reads the next column's data
-// while it computes one, and the k_waves partial sums are joined in LDS in
-// wave order. Up to 16 * NT tokens.
-template <uint32_t W, uint32_t X, uint32_t S, bool Z, int NT, int R>
+// of tiles and every k_waves-th column of tiles; D columns of its data are on
+// their way while it computes, and the k_waves partial sums are joined in LDS
+// in wave order.
+//
+// TP tokens share a matrix instruction's 16 rows of A: with TP < 16 row m
+// holds token m % TP and piece m / TP of every 16 / TP pieces, so that one
+// load brings several pieces and few tokens cost few loads (one token of bf16
+// took 4 loads a tile, each as large as the codes' own, and bounded the
+// kernel). Every piece's instruction then computes all rows, of which those of
+// its own piece are kept: rows 4 quarter + i are registers i of a quarter
+// wave, so a lane keeps the sums of piece (4 quarter) / TP and scales them by
+// that piece's group; the pieces are added up in the epilogue. NT > 1 (TP =
+// 16): up to 16 * NT tokens.
+template <uint32_t W, uint32_t X, uint32_t S, bool Z, int TP, int NT, int R, int D>
 __global__ void __launch_bounds__(64 * kWaves) k_w4(W4Launch a) {
+    typedef Kind<W, X, S, Z> K;
+    constexpr uint32_t XB = X == EQ_DTYPE_BF16 ? 2 : 1;
+    constexpr uint32_t LJ = 16 / TP;                      // pieces per load
+    constexpr uint32_t NL = K::Q / LJ;                    // loads per tile
+    constexpr uint32_t F = K::PG > LJ ? K::PG / LJ : 1;   // loads that share a lane's group
+    static_assert(NL >= 1 && NL % F == 0 && (NT == 1 || TP == 16), "tokens, pieces and groups fit");
     __shared__ f32x4 part[kWaves][R][64];
     const uint32_t wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), lane = threadIdx.x & 63u;
     const uint32_t i16 = lane & 15u, quarter = lane >> 4;
-    uint32_t ti = 0;
-    while (ti + 1 < a.n_tensors && blockIdx.x >= a.t[ti + 1].wg_begin) ++ti;
+    const uint32_t my_piece = 4 * quarter / TP;  // of a load's LJ, the one whose sums this lane keeps
+    const uint32_t ti = tensor_of(a, blockIdx.x);
     const W4Args &T = a.t[ti];
-    const uint32_t kw_n = T.k_waves, rw_n = kWaves / kw_n;
-    const uint32_t rw = wave / kw_n, kw = wave % kw_n;
-    const uint32_t row_tiles = (T.rows + kTileRows - 1) / kTileRows;
-    const uint32_t k_tiles = (T.cols + kTileCols - 1) / kTileCols, k_full = T.cols / kTileCols;
-    const uint32_t wg_tile = (blockIdx.x - T.wg_begin) * rw_n * R;
+    const uint32_t kw_n = 1u << T.kw_log2, rw_n = kWaves >> T.kw_log2;
+    const uint32_t rw = wave >> T.kw_log2, kw = wave & (kw_n - 1);
+    const uint32_t row_tiles = T.row_tiles, k_tiles = T.k_tiles, k_full = T.cols / kTileCols;
+    const uint32_t wg_tile = (blockIdx.x - a.wg_begin[ti]) * rw_n * R;
     const uint32_t token0 = blockIdx.y * kMaxTokens;
-    constexpr size_t XB = X == EQ_DTYPE_BF16 ? 2 : 1;
-    constexpr uint32_t P = kTileCols / S;
 
     const char *x_row[NT];
     for (int n = 0; n < NT; ++n) {
         // token rows past the end repeat the last one; their sums are not stored
-        uint32_t t = token0 + n * 16 + i16;
+        uint32_t t = token0 + n * 16 + i16 % TP;
         t = t < a.tokens ? t : a.tokens - 1;
         x_row[n] = static_cast<const char *>(T.x) + (uint64_t)t * T.ldx * XB;
     }
+    uint32_t x_col[NL];
+    for (uint32_t l = 0; l < NL; ++l) x_col[l] = K::col(quarter, l * LJ + i16 / TP);
     // rows of tiles past the end: the wave computes its R rows from the last
     // R that exist (R <= row_tiles, see the launcher), stores skip them
     uint32_t tile0 = wg_tile + rw * R;
     tile0 = tile0 + R <= row_tiles ? tile0 : row_tiles - R;
     const uint64_t base = (uint64_t)tile0 * k_tiles;
-    const u32x4 *codes = T.codes + base * 64 + lane;
-    const uint16_t *scales = T.scales + (base * 16 + i16) * P;
-    const uint8_t *zeros = Z ? T.zeros + (base * 16 + i16) * P : nullptr;
+
+    struct St {  // what the wave reads of one column of tiles
+        Weights<S, Z, R> w;
+        typename K::Raw x[NT][NL];
+    };
+    auto load = [&](St &st, uint32_t kt) {
+        st.w.load(T, base, kt, k_tiles, lane);
+#pragma unroll
+        for (int n = 0; n < NT; ++n)
+            for (uint32_t l = 0; l < NL; ++l)
+                st.x[n][l] = load_raw<X, typename K::Raw, true>(x_row[n] + ((uint64_t)kt * kTileCols + x_col[l]) * XB, 0);
+    };
+    auto load_tail = [&](St &st, uint32_t kt) {
+        st.w.load(T, base, kt, k_tiles, lane);
+#pragma unroll
+        for (int n = 0; n < NT; ++n)
+            for (uint32_t l = 0; l < NL; ++l) {
+                const uint32_t at = kt * kTileCols + x_col[l];
+                st.x[n][l] = load_raw<X, typename K::Raw, false>(x_row[n] + (uint64_t)at * XB, (int32_t)(T.cols - at));
+            }
+    };
 
     f32x4 acc[NT][R] = {};
-    using St = Stage<X, S, Z, NT, R>;
-    auto load = [&](St &st, uint32_t kt) {
-        load_stage<X, S, Z, NT, R, true>(st, T, codes, scales, zeros, x_row, kt, k_tiles, quarter);
+    auto compute = [&](const St &st) {
+#pragma unroll
+        for (uint32_t f = 0; f < NL / F; ++f) {
+            typename K::Sum d[NT][R][LJ] = {}, sx[NT] = {};
+#pragma unroll
+            for (uint32_t l = f * F; l < (f + 1) * F; ++l) {
+                typename K::Op xa[NT];
+#pragma unroll
+                for (int n = 0; n < NT; ++n) {
+                    xa[n] = K::acts(st.x[n][l]);
+                    if constexpr (K::kSumX) sx[n] = K::mma(xa[n], K::ones(), sx[n]);
+                }
+#pragma unroll
+                for (int r = 0; r < R; ++r)
+#pragma unroll
+                    for (uint32_t jj = 0; jj < LJ; ++jj) {
+                        const typename K::Op b = K::codes(st.w.c[r], l * LJ + jj);
+#pragma unroll
+                        for (int n = 0; n < NT; ++n) d[n][r][jj] = K::mma(xa[n], b, d[n][r][jj]);
+                    }
+            }
+            // the lane's group: the same for all lanes, or by its piece
+            const uint32_t g = (f * F * LJ + (LJ > K::PG ? my_piece : 0)) / K::PG;
+#pragma unroll
+            for (int r = 0; r < R; ++r) {
+                const float s = st.w.scale(r, g) * K::kScale, zero = st.w.zero(r, g);
+#pragma unroll
+                for (int n = 0; n < NT; ++n)
+                    for (int i = 0; i < 4; ++i) {
+                        auto v = d[n][r][0][i];
+                        if constexpr (LJ == 2) v = my_piece ? d[n][r][1][i] : v;
+                        if constexpr (LJ == 4) {
+                            v = my_piece == 1 ? d[n][r][1 % LJ][i] : v;
+                            v = my_piece == 2 ? d[n][r][2 % LJ][i] : v;
+                            v = my_piece == 3 ? d[n][r][3 % LJ][i] : v;
+                        }
+                        acc[n][r][i] = fmaf(s, K::value(v, sx[n][i], zero), acc[n][r][i]);
+                    }
+            }
+        }
     };
-    uint32_t left = k_full > kw ? (k_full - kw + kw_n - 1) / kw_n : 0;  // whole tiles of this wave
-    uint32_t kt = kw;
-    if (left) {
-        St st0, st1;
-        load(st0, kt);
-        while (left > 2) {
-            load(st1, kt + kw_n);
-            compute<W>(st0, acc);
-            load(st0, kt + 2 * kw_n);
-            compute<W>(st1, acc);
-            kt += 2 * kw_n;
-            left -= 2;
+
+    const uint32_t n_tiles = k_full > kw ? (k_full - kw + kw_n - 1) >> T.kw_log2 : 0;  // whole tiles of this wave
+    if (n_tiles) {
+        St st[D];
+        // a tile past the last is the last again: it is not computed
+        auto column = [&](uint32_t i) { return kw + ((i < n_tiles ? i : n_tiles - 1) << T.kw_log2); };
+#pragma unroll
+        for (uint32_t d = 0; d < D; ++d) load(st[d], column(d));
+        uint32_t i = 0;
+        for (; i + D < n_tiles; i += D) {
+#pragma unroll
+            for (uint32_t d = 0; d < D; ++d) {
+                compute(st[d]);
+                __builtin_amdgcn_sched_barrier(0);
+                load(st[d], column(i + D + d));
+                __builtin_amdgcn_sched_barrier(0);
+            }
         }
-        if (left == 2) {
-            load(st1, kt + kw_n);
-            compute<W>(st0, acc);
-            compute<W>(st1, acc);
-        } else {
-            compute<W>(st0, acc);
-        }
+#pragma unroll
+        for (uint32_t d = 0; d < D; ++d)
+            if (i + d < n_tiles) compute(st[d]);
     }
-    if (k_full < k_tiles && k_full % kw_n == kw) {  // the ragged last tile
+    if (k_full < k_tiles && (k_full & (kw_n - 1)) == kw) {  // the ragged last tile
         St st;
-        load_stage<X, S, Z, NT, R, false>(st, T, codes, scales, zeros, x_row, k_full, k_tiles, quarter);
-        compute<W>(st, acc);
+        load_tail(st, k_full);
+        compute(st);
     }
 
 #pragma unroll
@@ -364,49 +432,207 @@ __global__ void __launch_bounds__(64 * kWaves) k_w4(W4Launch a) {
         __syncthreads();
         for (uint32_t o = wave; o < rw_n * R; o += kWaves) {
             const uint32_t orw = o / R, r = o % R;
-            f32x4 s = part[orw * kw_n][r][lane];
-            for (uint32_t w = 1; w < kw_n; ++w) s += part[orw * kw_n + w][r][lane];
             uint32_t t0 = wg_tile + orw * R;
             const bool moved = t0 + R > row_tiles;
             if (moved && (t0 >= row_tiles || row_tiles - R + r < t0)) continue;  // another wave's row of tiles
             if (moved) t0 = row_tiles - R;
+            if (4 * quarter >= TP) continue;  // lanes of the first piece add up the others'
+            f32x4 s = {};
+            for (uint32_t w = 0; w < kw_n; ++w)
+                for (uint32_t jj = 0; jj < LJ; ++jj) s += part[orw * kw_n + w][r][lane + jj * 4 * TP];
             const uint32_t row = (t0 + r) * kTileRows + i16;
             for (int i = 0; i < 4; ++i) {
                 const uint32_t t = token0 + n * 16 + quarter * 4 + i;
                 if (t < a.tokens && row < T.rows) {
                     float v = s[i];
                     if constexpr (X != EQ_DTYPE_BF16) v *= T.x_scale[t];
-                    if (a.y_f32) static_cast<float *>(T.y)[t * T.ldy + row] = v;
-                    else static_cast<uint16_t *>(T.y)[t * T.ldy + row] = (uint16_t)pack_bf16(v, 0.0f);
+                    store_y(T, a.y_f32, t, row, v);
                 }
             }
         }
     }
 }
 
+// Many rows and more than a few tokens: the activations, read by every row of
+// tiles, outweigh the codes (64 tokens of int8 are 8 KiB a column of tiles
+// against R KiB of codes), so the 8 waves of a workgroup, R rows of tiles
+// each, share them: a chunk of kChunkTiles columns of tiles is put in LDS as
+// matrix operands while the chunk before it is computed (two buffers, one
+// barrier a chunk), and the codes of a whole chunk are on their way.
+constexpr uint32_t kChunkTiles = 4;
+
+template <uint32_t W, uint32_t X, uint32_t S, bool Z, int NT, int R>
+__global__ void __launch_bounds__(64 * kWaves) k_w4_wide(W4Launch a) {
+    // KS: how a lane loads activations; K: how it multiplies
+    typedef Kind<W, X, S, Z> KS;
+    typedef Kind<W, X == EQ_DTYPE_E4M3 ? EQ_DTYPE_BF16 : X, S, Z> K;
+    constexpr uint32_t XB = X == EQ_DTYPE_BF16 ? 2 : 1;
+    constexpr uint32_t P = kTileCols / S, C = kChunkTiles;
+    constexpr uint32_t kOps = K::Q / KS::Q;            // operands from one load (1, or 2 for E4M3 x 64)
+    constexpr uint32_t kLoads = C * NT * KS::Q / kWaves;  // a wave's loads for a chunk
+    static_assert(kLoads >= 1 && C * NT * KS::Q % kWaves == 0, "waves share out a chunk's loads evenly");
+    __shared__ typename K::Op xs[2][C][NT][K::Q][64];
+    const uint32_t wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), lane = threadIdx.x & 63u;
+    const uint32_t i16 = lane & 15u, quarter = lane >> 4;
+    const uint32_t ti = tensor_of(a, blockIdx.x);
+    const W4Args &T = a.t[ti];
+    const uint32_t row_tiles = T.row_tiles, k_tiles = T.k_tiles;
+    const uint32_t chunks = T.cols / (C * kTileCols);  // whole ones
+    const uint32_t token0 = blockIdx.y * kMaxTokens;
+    const uint32_t want = ((blockIdx.x - a.wg_begin[ti]) * kWaves + wave) * R;  // as in k_w4
+    const uint32_t tile0 = want + R <= row_tiles ? want : row_tiles - R;
+    const uint64_t base = (uint64_t)tile0 * k_tiles;
+
+    // the wave's loads of a chunk: (tile, token tile, piece) triples
+    const char *x_at[kLoads];
+    uint32_t x_col[kLoads], x_to[kLoads];
+    for (uint32_t i = 0; i < kLoads; ++i) {
+        const uint32_t k = wave * kLoads + i, p = k % KS::Q, n = k / KS::Q % NT, tile = k / KS::Q / NT;
+        uint32_t t = token0 + n * 16 + i16;
+        t = t < a.tokens ? t : a.tokens - 1;
+        x_col[i] = tile * kTileCols + KS::col(quarter, p);
+        x_at[i] = static_cast<const char *>(T.x) + ((uint64_t)t * T.ldx + x_col[i]) * XB;
+        x_to[i] = (tile * NT + n) * K::Q + p * kOps;
+    }
+    typename KS::Raw raw[kLoads];
+    auto load_x = [&](uint32_t chunk) {
+        for (uint32_t i = 0; i < kLoads; ++i)
+            raw[i] = load_raw<X, typename KS::Raw, true>(x_at[i] + (uint64_t)chunk * (C * kTileCols * XB), 0);
+    };
+    auto put_x = [&](uint32_t buf) {
+        typename K::Op(*to)[64] = &xs[buf][0][0][0];
+        for (uint32_t i = 0; i < kLoads; ++i) {
+            const auto o = KS::acts(raw[i]);
+            if constexpr (kOps == 2) {
+                to[x_to[i]][lane] = o.h[0];
+                to[x_to[i] + 1][lane] = o.h[1];
+            } else {
+                to[x_to[i]][lane] = o;
+            }
+        }
+    };
+
+    f32x4 acc[NT][R] = {};
+    auto compute = [&](const Weights<S, Z, R> &w, uint32_t buf, uint32_t tile) {
+#pragma unroll
+        for (uint32_t g = 0; g < P; ++g) {
+            typename K::Op b[K::PG][R], xa[2][K::PG];
+            float s[R], zero[R];
+            auto fetch = [&](int n) {
+                for (uint32_t p = 0; p < K::PG; ++p) xa[n & 1][p] = xs[buf][tile][n][g * K::PG + p][lane];
+                __builtin_amdgcn_sched_barrier(0);
+            };
+            fetch(0);
+#pragma unroll
+            for (int r = 0; r < R; ++r) {
+                for (uint32_t p = 0; p < K::PG; ++p) b[p][r] = K::codes(w.c[r], g * K::PG + p);
+                s[r] = w.scale(r, g) * K::kScale;
+                zero[r] = w.zero(r, g);
+            }
+            // one token tile's sums are scaled while the next one's products run
+            typename K::Sum d[2][R], sx[2];
+#pragma unroll
+            for (int n = 0; n <= NT; ++n) {
+                if (n + 1 < NT) fetch(n + 1);
+                if (n < NT) {
+                    sx[n & 1] = typename K::Sum{};
+                    for (int r = 0; r < R; ++r) d[n & 1][r] = typename K::Sum{};
+                    for (uint32_t p = 0; p < K::PG; ++p) {
+                        if constexpr (K::kSumX) sx[n & 1] = K::mma(xa[n & 1][p], K::ones(), sx[n & 1]);
+                        for (int r = 0; r < R; ++r) d[n & 1][r] = K::mma(xa[n & 1][p], b[p][r], d[n & 1][r]);
+                    }
+                }
+                if (n > 0)
+                    for (int r = 0; r < R; ++r)
+                        for (int i = 0; i < 4; ++i)
+                            acc[n - 1][r][i] = fmaf(s[r], K::value(d[~n & 1][r][i], sx[~n & 1][i], zero[r]), acc[n - 1][r][i]);
+            }
+        }
+    };
+
+    Weights<S, Z, R> w[C];
+    const uint32_t ragged = chunks * C;  // first column of tiles of the last, short chunk
+    auto load_w = [&](Weights<S, Z, R> &d, uint32_t kt) { d.load(T, base, kt < k_tiles ? kt : k_tiles - 1, k_tiles, lane); };
+#pragma unroll
+    for (uint32_t d = 0; d < C; ++d) load_w(w[d], d);
+    if (chunks) {
+        load_x(0);
+        put_x(0);
+    }
+    __syncthreads();
+    // All workgroups walk the columns in the same order: the activations of a
+    // chunk are then in L2 for all of them (started at different chunks, they
+    // took 15% longer). The fences keep loads where they are issued: moved
+    // down to the end of a chunk they were waited for at the start of the next.
+    for (uint32_t ch = 0; ch < chunks; ++ch) {
+        load_x(ch + 1 < chunks ? ch + 1 : ch);  // the last one again: not used
+        __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+        for (uint32_t d = 0; d < C; ++d) {
+            compute(w[d], ch & 1, d);
+            __builtin_amdgcn_sched_barrier(0);
+            load_w(w[d], (ch + 1) * C + d);
+            __builtin_amdgcn_sched_barrier(0);
+        }
+        put_x(~ch & 1);
+        __syncthreads();
+    }
+    if (ragged < k_tiles) {
+        for (uint32_t i = 0; i < kLoads; ++i)
+            raw[i] = load_raw<X, typename KS::Raw, false>(x_at[i] + (uint64_t)ragged * (kTileCols * XB),
+                                                          (int32_t)(T.cols - ragged * kTileCols) - (int32_t)x_col[i]);
+        put_x(0);
+        __syncthreads();
+#pragma unroll
+        for (uint32_t d = 0; d < C; ++d)
+            if (ragged + d < k_tiles) compute(w[d], 0, d);
+    }
+#pragma unroll
+    for (int r = 0; r < R; ++r) {
+        const uint32_t row = (tile0 + r) * kTileRows + i16;
+        if (tile0 + r < want || row >= T.rows) continue;  // another wave's row of tiles, or none
+#pragma unroll
+        for (int n = 0; n < NT; ++n)
+            for (int i = 0; i < 4; ++i) {
+                const uint32_t t = token0 + n * 16 + quarter * 4 + i;
+                if (t < a.tokens) store_y(T, a.y_f32, t, row, X == EQ_DTYPE_BF16 ? acc[n][r][i] : acc[n][r][i] * T.x_scale[t]);
+            }
+    }
+}
+
 typedef void (*W4Fn)(W4Launch);
 
 template <uint32_t W, uint32_t X, bool Z, uint32_t S>
-W4Fn pick_shape(uint32_t nt, uint32_t r) {
-    if (nt == 1) return r == 1 ? k_w4<W, X, S, Z, 1, 1> : k_w4<W, X, S, Z, 1, 2>;
-    if (nt == 2) return r == 1 ? k_w4<W, X, S, Z, 2, 1> : k_w4<W, X, S, Z, 2, 2>;
-    return r == 1 ? k_w4<W, X, S, Z, 4, 1> : k_w4<W, X, S, Z, 4, 2>;
+W4Fn pick_shape(uint32_t nt, uint32_t tp, uint32_t r, bool wide) {
+    if (wide) {
+        if (nt == 1) return r == 1 ? k_w4_wide<W, X, S, Z, 1, 1> : k_w4_wide<W, X, S, Z, 1, 2>;
+        if (nt == 2) return r == 1 ? k_w4_wide<W, X, S, Z, 2, 1> : k_w4_wide<W, X, S, Z, 2, 2>;
+        return r == 1 ? k_w4_wide<W, X, S, Z, 4, 1> : k_w4_wide<W, X, S, Z, 4, 2>;
+    }
+    if (tp == 4) {
+        if constexpr (Kind<W, X, S, Z>::Q == 4) return k_w4<W, X, S, Z, 4, 1, 1, 4>;
+        tp = 8;
+    }
+    if (tp == 8) return r == 1 ? k_w4<W, X, S, Z, 8, 1, 1, 4> : k_w4<W, X, S, Z, 8, 1, 2, 2>;
+    if (nt == 1) return r == 1 ? k_w4<W, X, S, Z, 16, 1, 1, 2> : k_w4<W, X, S, Z, 16, 1, 2, 2>;
+    if (nt == 2) return r == 1 ? k_w4<W, X, S, Z, 16, 2, 1, 2> : k_w4<W, X, S, Z, 16, 2, 2, 2>;
+    return r == 1 ? k_w4<W, X, S, Z, 16, 4, 1, 2> : k_w4<W, X, S, Z, 16, 4, 2, 2>;
 }
 template <uint32_t W, uint32_t X, bool Z>
-W4Fn pick_group(uint32_t group, uint32_t nt, uint32_t r) {
-    if (group == 32) return pick_shape<W, X, Z, 32>(nt, r);
-    if (group == 64) return pick_shape<W, X, Z, 64>(nt, r);
-    return pick_shape<W, X, Z, 128>(nt, r);
+W4Fn pick_group(uint32_t group, uint32_t nt, uint32_t tp, uint32_t r, bool wide) {
+    if (group == 32) return pick_shape<W, X, Z, 32>(nt, tp, r, wide);
+    if (group == 64) return pick_shape<W, X, Z, 64>(nt, tp, r, wide);
+    return pick_shape<W, X, Z, 128>(nt, tp, r, wide);
 }
-W4Fn pick(uint32_t w, uint32_t x, bool z, uint32_t group, uint32_t nt, uint32_t r) {
+W4Fn pick(uint32_t w, uint32_t x, bool z, uint32_t group, uint32_t nt, uint32_t tp, uint32_t r, bool wide) {
     if (w == EQ_DTYPE_E2M1)
-        return x == EQ_DTYPE_BF16 ? pick_group<EQ_DTYPE_E2M1, EQ_DTYPE_BF16, false>(group, nt, r)
-                                  : pick_group<EQ_DTYPE_E2M1, EQ_DTYPE_E4M3, false>(group, nt, r);
+        return x == EQ_DTYPE_BF16 ? pick_group<EQ_DTYPE_E2M1, EQ_DTYPE_BF16, false>(group, nt, tp, r, wide)
+                                  : pick_group<EQ_DTYPE_E2M1, EQ_DTYPE_E4M3, false>(group, nt, tp, r, wide);
     if (x == EQ_DTYPE_BF16)
-        return z ? pick_group<EQ_DTYPE_INT4, EQ_DTYPE_BF16, true>(group, nt, r)
-                 : pick_group<EQ_DTYPE_INT4, EQ_DTYPE_BF16, false>(group, nt, r);
-    return z ? pick_group<EQ_DTYPE_INT4, EQ_DTYPE_INT8, true>(group, nt, r)
-             : pick_group<EQ_DTYPE_INT4, EQ_DTYPE_INT8, false>(group, nt, r);
+        return z ? pick_group<EQ_DTYPE_INT4, EQ_DTYPE_BF16, true>(group, nt, tp, r, wide)
+                 : pick_group<EQ_DTYPE_INT4, EQ_DTYPE_BF16, false>(group, nt, tp, r, wide);
+    return z ? pick_group<EQ_DTYPE_INT4, EQ_DTYPE_INT8, true>(group, nt, tp, r, wide)
+             : pick_group<EQ_DTYPE_INT4, EQ_DTYPE_INT8, false>(group, nt, tp, r, wide);
 }
 
 // Row-major codes, scales and zeros to tiles: one thread per 4-byte word of
@@ -458,22 +684,24 @@ bool tensor_ok(const eq_w4_tensor &t) {
 }
 
 struct Shape {
-    uint32_t nt, r;  // token tiles of 16 and rows of tiles per wave
+    uint32_t nt, tp, r;  // token tiles of tp (4, 8 or 16) tokens and rows of tiles per wave
+    bool wide;           // k_w4_wide
 };
 
 // R: rows of tiles that share a wave's activations.
 Shape shape(uint64_t tokens, uint64_t row_tiles, uint64_t fewest) {
     const uint32_t nt = tokens <= 16 ? 1 : tokens <= 32 ? 2 : 4;
     uint32_t r = tokens > 4 ? 2 : 1;
-    while (r > 1 && (row_tiles < 512 * r || fewest < r)) r /= 2;
-    return {nt, r};
+    while (r > 1 && (row_tiles < 128 * r || fewest < r)) r /= 2;
+    const bool wide = tokens > 8 && row_tiles >= (nt == 1 ? 1536 : nt == 2 ? 1024 : 640) && fewest >= 2;
+    if (wide) r = row_tiles >= 2560 ? 2 : 1;
+    return {nt, tokens <= 4 ? 4u : tokens <= 8 ? 8u : 16u, r, wide};
 }
 
-// Waves that share out the columns: as many as have two tiles each.
-uint32_t k_waves(uint64_t cols) {
-    const uint64_t k_tiles = (cols + kTileCols - 1) / kTileCols;
-    uint32_t n = kWaves;
-    while (n > 1 && k_tiles < 2 * n) n /= 2;
+// Waves that share out the columns (log2): as many as have two tiles each.
+uint32_t kw_log2(uint32_t k_tiles) {
+    uint32_t n = 3;
+    while (n > 0 && k_tiles < (2u << n)) --n;
     return n;
 }
 
@@ -484,6 +712,8 @@ W4Args tensor_args(const eq_w4_tensor &t) {
     a.zeros = t.d_zeros;
     a.rows = (uint32_t)t.rows;
     a.cols = (uint32_t)t.cols;
+    a.k_tiles = (uint32_t)((t.cols + kTileCols - 1) / kTileCols);
+    a.row_tiles = (uint32_t)((t.rows + kTileRows - 1) / kTileRows);
     a.group = t.group;
     return a;
 }
@@ -553,26 +783,28 @@ eq_status eq_w4_matvec(const eq_w4_tensor *tensors, uint32_t n_tensors, const eq
         const Shape sh = shape(tokens, total, fewest);
         W4Launch a{};
         uint64_t wgs = 0;
-        for (; a.n_tensors < n; ++a.n_tensors) {
-            const uint32_t i = which[a.n_tensors];
-            W4Args &t = a.t[a.n_tensors];
+        for (uint32_t k = 0; k < EQ_MAX_BLOCK_TENSORS; ++k) a.wg_begin[k] = ~0u;
+        for (uint32_t k = 0; k < n; ++k) {
+            const uint32_t i = which[k];
+            W4Args &t = a.t[k];
             t = tensor_args(tensors[i]);
             t.x = x[i].d;
             t.x_scale = x[i].d_scale;
             t.y = y[i].d;
             t.ldx = x[i].stride;
             t.ldy = y[i].stride;
-            t.wg_begin = (uint32_t)wgs;
-            t.k_waves = k_waves(tensors[i].cols);
-            const uint64_t per_wg = kWaves / t.k_waves * sh.r * kTileRows;
-            wgs += (tensors[i].rows + per_wg - 1) / per_wg;
+            if (wgs > kMaxThreads / (64 * kWaves)) return EQ_EINVAL;
+            a.wg_begin[k] = (uint32_t)wgs;
+            t.kw_log2 = sh.wide ? 0 : kw_log2(t.k_tiles);
+            const uint64_t per_wg = (kWaves >> t.kw_log2) * sh.r;
+            wgs += (t.row_tiles + per_wg - 1) / per_wg;
         }
         const uint64_t passes = (tokens + kMaxTokens - 1) / kMaxTokens;
         if (wgs > kMaxThreads / (64 * kWaves)) return EQ_EINVAL;
         a.tokens = (uint32_t)tokens;
         a.y_f32 = y[first].dtype == EQ_DTYPE_F32;
         hipLaunchKernelGGL(pick(tensors[first].dtype, x[first].dtype, tensors[first].d_zeros != nullptr,
-                                tensors[first].group, sh.nt, sh.r),
+                                tensors[first].group, sh.nt, sh.tp, sh.r, sh.wide),
                            dim3((uint32_t)wgs, (uint32_t)passes), dim3(64 * kWaves), 0,
                            static_cast<hipStream_t>(stream), a);
         if (hipGetLastError() != hipSuccess) return EQ_EHIP;

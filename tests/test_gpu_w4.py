@@ -142,6 +142,15 @@ def test_larger_shapes_exact(kind, zeros, xt):
 
 
 @pytest.mark.parametrize("kind,zeros,xt", KINDS)
+@pytest.mark.parametrize("group", [32, 64, 128])
+def test_many_rows_exact(kind, zeros, xt, group):
+    """Enough rows that a workgroup's waves share the activations: chunks of 512 columns, none to several of them, whole and ragged."""
+    for i, (tokens, cols) in enumerate([(9, 100), (16, 512), (17, 640), (32, 1111), (33, 1024), (64, 1700), (80, 513)]):
+        run(9000 + 20 * i + group, tokens, [25000, 40], cols, kind, zeros, xt, group, strides=i % 2 == 0, yt=F32 if i else BF16)
+    run(9500 + group, 48, [30001], 256, kind, zeros, xt, group, exact=False)
+
+
+@pytest.mark.parametrize("kind,zeros,xt", KINDS)
 def test_single_columns(kind, zeros, xt):
     """x with one 1 per token picks single weights: the layout, column by column."""
     cols, rows, group = 200, 21, 64
@@ -241,8 +250,11 @@ def test_pack_layout():
         zs = t.zeros.cpu().numpy().reshape(scales.shape) if zeros else None
         for r in range(16 * -(-rows // 16)):
             for c in range(128 * k_tiles):
-                quarter, within = c % group // (group // 4), c % group % (group // 4)
-                word = int(words[r // 16, c // 128, quarter, r % 16, (c % 128 // group * (group // 4) + within) // 8])
+                if group == 32:
+                    quarter, j = c % 32 // 8, c % 128 // 32
+                else:
+                    quarter, j = c % 64 // 16, c % 128 // 64 * 2 + c % 16 // 8
+                word = int(words[r // 16, c // 128, quarter, r % 16, j])
                 got = word >> 4 * place.index(c % 8) & 15
                 assert got == (int(w.codes[r, c]) if r < rows and c < cols else 0)
             for g in range(k_tiles * per):
