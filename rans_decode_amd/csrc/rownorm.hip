@@ -48,73 +48,70 @@ struct RowArgs {
     float eps;
 };
 
-// 8 consecutive values of a row of bf16 or fp32, of which `left` exist (the
-// rest read as zero).
+// 8 consecutive values of a row of bf16 or fp32.
 template <bool F32>
-__device__ __forceinline__ void load8(const void *row, uint32_t at, uint32_t left, float (&v)[kChunk]) {
+__device__ __forceinline__ void load8(const void *row, uint32_t at, float (&v)[kChunk]) {
     if constexpr (F32) {
         const float *p = static_cast<const float *>(row) + at;
-        if (left >= kChunk) {
-            const f32x4 a = *reinterpret_cast<const f32x4_a4 *>(p), b = *reinterpret_cast<const f32x4_a4 *>(p + 4);
-            for (int i = 0; i < 4; ++i) v[i] = a[i], v[4 + i] = b[i];
-        } else {
-            for (uint32_t i = 0; i < kChunk; ++i) v[i] = i < left ? p[i] : 0.0f;
-        }
+        const f32x4 a = *reinterpret_cast<const f32x4_a4 *>(p), b = *reinterpret_cast<const f32x4_a4 *>(p + 4);
+        for (int i = 0; i < 4; ++i) v[i] = a[i], v[4 + i] = b[i];
     } else {
-        const uint16_t *p = static_cast<const uint16_t *>(row) + at;
-        if (left >= kChunk) {
-            const u32x4 a = *reinterpret_cast<const u32x4_a2 *>(p);
-            for (int i = 0; i < 4; ++i) v[2 * i] = bf16_lo(a[i]), v[2 * i + 1] = bf16_hi(a[i]);
-        } else {
-            for (uint32_t i = 0; i < kChunk; ++i) v[i] = i < left ? bf16_val(p[i]) : 0.0f;
-        }
+        const u32x4 a = *reinterpret_cast<const u32x4_a2 *>(static_cast<const uint16_t *>(row) + at);
+        for (int i = 0; i < 4; ++i) v[2 * i] = bf16_lo(a[i]), v[2 * i + 1] = bf16_hi(a[i]);
     }
 }
 
-__device__ __forceinline__ void store_bf16(void *row, uint32_t at, uint32_t left, const float (&v)[kChunk]) {
-    uint16_t *p = static_cast<uint16_t *>(row) + at;
+// One value as stored, and as a number.
+template <bool F32>
+__device__ __forceinline__ uint32_t load_bits(const void *row, uint32_t at) {
+    return F32 ? static_cast<const uint32_t *>(row)[at] : static_cast<const uint16_t *>(row)[at];
+}
+template <bool F32>
+__device__ __forceinline__ float from_bits(uint32_t b) {
+    return __uint_as_float(F32 ? b : b << 16);
+}
+
+__device__ __forceinline__ uint32_t bf16_bits(float v) { return pack_bf16(v, 0.0f) & 0xFFFFu; }
+
+__device__ __forceinline__ void store8_bf16(void *row, uint32_t at, const float (&v)[kChunk]) {
     u32x4 a;
     for (int i = 0; i < 4; ++i) a[i] = pack_bf16(v[2 * i], v[2 * i + 1]);
-    if (left >= kChunk) {
-        *reinterpret_cast<u32x4_a2 *>(p) = a;
-    } else {
-        for (uint32_t i = 0; i < kChunk; ++i)
-            if (i < left) p[i] = (uint16_t)(a[i / 2] >> (16 * (i & 1)));
-    }
+    *reinterpret_cast<u32x4_a2 *>(static_cast<uint16_t *>(row) + at) = a;
 }
 
-__device__ __forceinline__ void store_f32(void *row, uint32_t at, uint32_t left, const float (&v)[kChunk]) {
+__device__ __forceinline__ void store8_f32(void *row, uint32_t at, const float (&v)[kChunk]) {
     float *p = static_cast<float *>(row) + at;
-    if (left >= kChunk) {
-        *reinterpret_cast<f32x4_a4 *>(p) = f32x4{v[0], v[1], v[2], v[3]};
-        *reinterpret_cast<f32x4_a4 *>(p + 4) = f32x4{v[4], v[5], v[6], v[7]};
+    *reinterpret_cast<f32x4_a4 *>(p) = f32x4{v[0], v[1], v[2], v[3]};
+    *reinterpret_cast<f32x4_a4 *>(p + 4) = f32x4{v[4], v[5], v[6], v[7]};
+}
+
+// Four 8-bit codes. |t| <= L * (1 + 2^-23), which rounds to L.
+template <uint32_t OUT>
+__device__ __forceinline__ uint32_t codes4(float t0, float t1, float t2, float t3) {
+    if constexpr (OUT == EQ_DTYPE_INT8) {
+        return ((uint32_t)(int32_t)rintf(t0) & 255u) | ((uint32_t)(int32_t)rintf(t1) & 255u) << 8 |
+               ((uint32_t)(int32_t)rintf(t2) & 255u) << 16 | (uint32_t)(int32_t)rintf(t3) << 24;
     } else {
-        for (uint32_t i = 0; i < kChunk; ++i)
-            if (i < left) p[i] = v[i];
+        const int a = __builtin_amdgcn_cvt_pk_fp8_f32(t0, t1, 0, false);
+        return (uint32_t)__builtin_amdgcn_cvt_pk_fp8_f32(t2, t3, a, true);
     }
 }
 
-// 8-bit codes of v * inv. |v * inv| <= L * (1 + 2^-23), which rounds to L.
+// v * inv as codes (8-bit types) or v as bf16.
 template <uint32_t OUT>
-__device__ __forceinline__ void store_8bit(void *row, uint32_t at, uint32_t left, const float (&v)[kChunk], float inv) {
-    uint8_t *p = static_cast<uint8_t *>(row) + at;
-    uint32_t a[2];
-    for (int h = 0; h < 2; ++h) {
-        const float *t = v + 4 * h;
-        if constexpr (OUT == EQ_DTYPE_INT8) {
-            a[h] = 0;
-            for (int i = 0; i < 4; ++i) a[h] |= ((uint32_t)(int32_t)rintf(t[i] * inv) & 255u) << (8 * i);
-        } else {
-            a[h] = (uint32_t)__builtin_amdgcn_cvt_pk_fp8_f32(t[0] * inv, t[1] * inv, 0, false);
-            a[h] = (uint32_t)__builtin_amdgcn_cvt_pk_fp8_f32(t[2] * inv, t[3] * inv, (int)a[h], true);
-        }
-    }
-    if (left >= kChunk) {
-        *reinterpret_cast<u32x2_a1 *>(p) = u32x2{a[0], a[1]};
+__device__ __forceinline__ void store8(void *row, uint32_t at, const float (&v)[kChunk], float inv) {
+    if constexpr (OUT == EQ_DTYPE_BF16) {
+        store8_bf16(row, at, v);
     } else {
-        for (uint32_t i = 0; i < kChunk; ++i)
-            if (i < left) p[i] = (uint8_t)(a[i / 4] >> (8 * (i & 3)));
+        const u32x2 a = {codes4<OUT>(v[0] * inv, v[1] * inv, v[2] * inv, v[3] * inv),
+                         codes4<OUT>(v[4] * inv, v[5] * inv, v[6] * inv, v[7] * inv)};
+        *reinterpret_cast<u32x2_a1 *>(static_cast<uint8_t *>(row) + at) = a;
     }
+}
+template <uint32_t OUT>
+__device__ __forceinline__ void store1(void *row, uint32_t at, float v, float inv) {
+    if constexpr (OUT == EQ_DTYPE_BF16) static_cast<uint16_t *>(row)[at] = (uint16_t)bf16_bits(v);
+    else static_cast<uint8_t *>(row)[at] = (uint8_t)codes4<OUT>(v * inv, 0.0f, 0.0f, 0.0f);
 }
 
 // One step of a wave reduction: every lane joins the value of its partner.
@@ -159,73 +156,121 @@ __device__ __forceinline__ void reduce(float &sum, uint32_t &top, float *lds_sum
 
 enum Op : uint32_t { NORM, SILU };
 
+__device__ __forceinline__ float silu(float g) { return g * __builtin_amdgcn_rcpf(1.0f + __expf(-g)); }
+
+__device__ __forceinline__ void join_top(uint32_t &top, float v) {
+    const uint32_t b = __float_as_uint(v) & 0x7FFFFFFFu;
+    top = top > b ? top : b;
+}
+
 // The row's values before its common factor: s * w (norm, squares of s added
 // to sum) or the finished y (silu); top joins the patterns of their |value|.
-template <uint32_t OP, bool XF32, uint32_t RES>  // RES: 0 none, else EQ_DTYPE_BF16 / EQ_DTYPE_F32
-__device__ __forceinline__ void values8(const RowArgs &a, uint64_t row, uint32_t at, float (&v)[kChunk],
-                                        float &sum, uint32_t &top) {
-    const uint32_t left = a.cols - at;
-    constexpr size_t XB = XF32 ? 4 : 2;
-    load8<XF32>(static_cast<const char *>(a.x) + row * a.ldx * XB, at, left, v);
-    if constexpr (OP == SILU) {
-        float u[kChunk];
-        load8<XF32>(static_cast<const char *>(a.r) + row * a.ldr * XB, at, left, u);
-        for (uint32_t i = 0; i < kChunk; ++i) v[i] = v[i] * __builtin_amdgcn_rcpf(1.0f + __expf(-v[i])) * u[i];
-    } else {
-        if constexpr (RES != 0) {
-            constexpr bool RF32 = RES == EQ_DTYPE_F32;
-            float r[kChunk];
-            load8<RF32>(static_cast<const char *>(a.r) + row * a.ldr * (RF32 ? 4 : 2), at, left, r);
-            for (uint32_t i = 0; i < kChunk; ++i) v[i] += r[i];
-            if constexpr (RF32) {
-                store_f32(static_cast<char *>(a.r_out) + row * a.ldro * 4, at, left, v);
-            } else {
-                store_bf16(static_cast<char *>(a.r_out) + row * a.ldro * 2, at, left, v);
-                // the norm is of the residual as it is stored
-                for (uint32_t i = 0; i < kChunk; i += 2) {
-                    const uint32_t p = pack_bf16(v[i], v[i + 1]);
-                    v[i] = bf16_lo(p);
-                    v[i + 1] = bf16_hi(p);
+// RES: 0 none, else EQ_DTYPE_BF16 / EQ_DTYPE_F32.
+template <uint32_t OP, bool XF32, uint32_t RES>
+struct Row {
+    static constexpr bool RF32 = OP == SILU ? XF32 : RES == EQ_DTYPE_F32;
+    static constexpr size_t XB = XF32 ? 4 : 2, RB = RF32 ? 4 : 2;
+    const char *x, *r;
+    char *r_out;
+    const void *w;
+    bool w_f32;
+
+    __device__ __forceinline__ Row(const RowArgs &a, uint64_t row)
+        : x(static_cast<const char *>(a.x) + row * a.ldx * XB), r(static_cast<const char *>(a.r) + row * a.ldr * RB),
+          r_out(static_cast<char *>(a.r_out) + row * a.ldro * RB), w(a.w), w_f32(a.w_f32) {}
+
+    __device__ __forceinline__ void values8(uint32_t at, float (&v)[kChunk], float &sum, uint32_t &top) const {
+        load8<XF32>(x, at, v);
+        if constexpr (OP == SILU) {
+            float u[kChunk];
+            load8<XF32>(r, at, u);
+            for (uint32_t i = 0; i < kChunk; ++i) v[i] = silu(v[i]) * u[i];
+        } else {
+            if constexpr (RES != 0) {
+                float t[kChunk];
+                load8<RF32>(r, at, t);
+                for (uint32_t i = 0; i < kChunk; ++i) v[i] += t[i];
+                if constexpr (RF32) {
+                    store8_f32(r_out, at, v);
+                } else {
+                    store8_bf16(r_out, at, v);
+                    // the norm is of the residual as it is stored
+                    for (uint32_t i = 0; i < kChunk; ++i) v[i] = from_bits<false>(bf16_bits(v[i]));
                 }
             }
+            for (uint32_t i = 0; i < kChunk; ++i) sum = fmaf(v[i], v[i], sum);
+            if (w) {
+                float t[kChunk];
+                if (w_f32) load8<true>(w, at, t);
+                else load8<false>(w, at, t);
+                for (uint32_t i = 0; i < kChunk; ++i) v[i] *= t[i];
+            }
         }
-        for (uint32_t i = 0; i < kChunk; ++i) sum = fmaf(v[i], v[i], sum);
-        if (a.w) {
-            float w[kChunk];
-            if (a.w_f32) load8<true>(a.w, at, left, w);
-            else load8<false>(a.w, at, left, w);
-            for (uint32_t i = 0; i < kChunk; ++i) v[i] *= w[i];
+        for (uint32_t i = 0; i < kChunk; ++i) join_top(top, v[i]);
+    }
+
+    // One value of the last, short chunk: its loads, and what is made of them.
+    struct Bits { uint32_t x, r, w; };
+    __device__ __forceinline__ Bits load1(uint32_t at) const {
+        Bits b = {load_bits<XF32>(x, at), 0, 0};
+        if constexpr (OP == SILU || RES != 0) b.r = load_bits<RF32>(r, at);
+        if constexpr (OP == NORM)
+            if (w) b.w = w_f32 ? load_bits<true>(w, at) : load_bits<false>(w, at) << 16;
+        return b;
+    }
+    __device__ __forceinline__ float value1(uint32_t at, Bits b, float &sum, uint32_t &top) const {
+        float v = from_bits<XF32>(b.x);
+        if constexpr (OP == SILU) {
+            v = silu(v) * from_bits<RF32>(b.r);
+        } else {
+            if constexpr (RES != 0) {
+                v += from_bits<RF32>(b.r);
+                if constexpr (RF32) {
+                    reinterpret_cast<float *>(r_out)[at] = v;
+                } else {
+                    const uint32_t h = bf16_bits(v);
+                    reinterpret_cast<uint16_t *>(r_out)[at] = (uint16_t)h;
+                    v = from_bits<false>(h);
+                }
+            }
+            sum = fmaf(v, v, sum);
+            if (w) v *= __uint_as_float(b.w);
         }
+        join_top(top, v);
+        return v;
     }
-    for (uint32_t i = 0; i < kChunk; ++i) {
-        const uint32_t b = __float_as_uint(v[i]) & 0x7FFFFFFFu;
-        top = top > b ? top : b;
-    }
-}
+};
 
 // NV chunks per thread in registers; NV = 0: rows of any length, whose values
 // are computed a second time for the output (norm: from the stored sum where
-// there is one, else from x).
+// there is one, else from x). The last cols % 8 values go to one thread each,
+// their loads ahead of the chunks' (a chunk of its own for them, filled value
+// by value, cost rows of 5003 bf16 20%).
 template <uint32_t OP, bool XF32, uint32_t RES, uint32_t OUT, int NV>
 __global__ void __launch_bounds__(kMaxThreads) k_row(RowArgs a) {
+    typedef Row<OP, XF32, RES> In;
     __shared__ float lds_sum[kMaxThreads / 64];
     __shared__ uint32_t lds_top[kMaxThreads / 64];
     const uint64_t row = (uint64_t)blockIdx.y * gridDim.x + blockIdx.x;
     if (row >= a.tokens) return;
+    const In in(a, row);
+    const uint32_t whole = a.cols / kChunk * kChunk;  // values in whole chunks
     const uint32_t step = blockDim.x * kChunk;
-    const uint32_t first = threadIdx.x * kChunk;
-    float v[NV ? NV : 1][kChunk];
+    const uint32_t first = threadIdx.x * kChunk, last = whole + threadIdx.x;
+    const bool extra = last < a.cols;
+    float v[NV ? NV : 1][kChunk], v1 = 0.0f;
     float sum = 0.0f;
     uint32_t top = 0;
+    typename In::Bits bits = {};
+    if (extra) bits = in.load1(last);
     if constexpr (NV > 0) {
 #pragma unroll
-        for (int i = 0; i < NV; ++i) {
-            const uint32_t at = first + i * step;
-            if (at < a.cols) values8<OP, XF32, RES>(a, row, at, v[i], sum, top);
-        }
+        for (int i = 0; i < NV; ++i)
+            if (first + i * step < whole) in.values8(first + i * step, v[i], sum, top);
     } else {
-        for (uint64_t at = first; at < a.cols; at += step) values8<OP, XF32, RES>(a, row, (uint32_t)at, v[0], sum, top);
+        for (uint64_t at = first; at < whole; at += step) in.values8((uint32_t)at, v[0], sum, top);
     }
+    if (extra) v1 = in.value1(last, bits, sum, top);
     float factor = 1.0f, inv = 1.0f;
     if constexpr (OP == NORM || OUT != EQ_DTYPE_BF16) {
         reduce(sum, top, lds_sum, lds_top);
@@ -243,27 +288,27 @@ __global__ void __launch_bounds__(kMaxThreads) k_row(RowArgs a) {
     auto finish = [&](uint32_t at, float(&t)[kChunk]) {
         if constexpr (OP == NORM)
             for (uint32_t i = 0; i < kChunk; ++i) t[i] *= factor;
-        if constexpr (OUT == EQ_DTYPE_BF16) store_bf16(out, at, a.cols - at, t);
-        else store_8bit<OUT>(out, at, a.cols - at, t, inv);
+        store8<OUT>(out, at, t, inv);
     };
     if constexpr (NV > 0) {
 #pragma unroll
-        for (int i = 0; i < NV; ++i) {
-            const uint32_t at = first + i * step;
-            if (at < a.cols) finish(at, v[i]);
-        }
+        for (int i = 0; i < NV; ++i)
+            if (first + i * step < whole) finish(first + i * step, v[i]);
     } else {
-        RowArgs again = a;
-        if constexpr (RES != 0) {  // each thread reads back what it wrote itself
-            again.x = a.r_out;
-            again.ldx = a.ldro;
+        // a norm's second pass reads back what this thread itself stored
+        typedef Row<OP, RES ? RES == EQ_DTYPE_F32 : XF32, 0> Again;
+        RowArgs b = a;
+        if constexpr (RES != 0) {
+            b.x = a.r_out;
+            b.ldx = a.ldro;
         }
-        constexpr bool XF = RES ? RES == EQ_DTYPE_F32 : XF32;
-        for (uint64_t at = first; at < a.cols; at += step) {
-            values8<OP, XF, 0>(again, row, (uint32_t)at, v[0], sum, top);
+        const Again again(b, row);
+        for (uint64_t at = first; at < whole; at += step) {
+            again.values8((uint32_t)at, v[0], sum, top);
             finish((uint32_t)at, v[0]);
         }
     }
+    if (extra) store1<OUT>(out, last, OP == NORM ? v1 * factor : v1, inv);
 }
 
 typedef void (*RowFn)(RowArgs);
@@ -273,6 +318,7 @@ RowFn pick_nv(int nv) {
     switch (nv) {
         case 1: return k_row<OP, XF32, RES, OUT, 1>;
         case 2: return k_row<OP, XF32, RES, OUT, 2>;
+        case 3: return k_row<OP, XF32, RES, OUT, 3>;
         case 4: return k_row<OP, XF32, RES, OUT, 4>;
         default: return k_row<OP, XF32, RES, OUT, 0>;
     }
@@ -310,14 +356,17 @@ eq_status launch_rows(RowFn fn, const RowArgs &a, uint64_t tokens, uint32_t thre
     return hipGetLastError() == hipSuccess ? EQ_OK : EQ_EHIP;
 }
 
-// Threads per row and chunks per thread.
-void shape(uint64_t cols, uint32_t *threads, int *nv) {
-    const uint64_t chunks = (cols + kChunk - 1) / kChunk;
+// Threads per row and chunks per thread. Few rows: a thread per chunk (512 rows
+// of 4096: 5.2 us, with three chunks a thread 5.9); many: up to three, so that
+// more rows are on their way at once (8192 rows of 8192, bf16 with residual to
+// E4M3: 90.3 us, one chunk 95.3, four 106.1; 1777 rows of 5000: 9.6, one 10.8).
+void shape(uint64_t tokens, uint64_t cols, uint32_t *threads, int *nv) {
+    const uint64_t chunks = (cols + kChunk - 1) / kChunk, most = tokens < 1024 ? 1 : 3;
     uint32_t t = 64;
-    while (t < kMaxThreads && t < chunks) t *= 2;
+    while (t < kMaxThreads && t * most < chunks) t *= 2;
     const uint64_t per = (chunks + t - 1) / t;
     *threads = t;
-    *nv = per <= 1 ? 1 : per <= 2 ? 2 : per <= 4 ? 4 : 0;
+    *nv = per <= 4 ? (int)per : 0;
 }
 
 }  // namespace
@@ -356,7 +405,7 @@ eq_status eq_add_rmsnorm(const eq_matrix *x, const eq_matrix *residual, const eq
     a.eps = eps;
     uint32_t threads;
     int nv;
-    shape(cols, &threads, &nv);
+    shape(tokens, cols, &threads, &nv);
     const uint32_t res = residual ? residual->dtype : 0;
     RowFn fn = x->dtype == EQ_DTYPE_F32 ? pick_res<true>(res, out->dtype, nv) : pick_res<false>(res, out->dtype, nv);
     return launch_rows(fn, a, tokens, threads, stream);
@@ -382,7 +431,7 @@ eq_status eq_silu_mul(const eq_matrix *gate, const eq_matrix *up, uint64_t token
     a.tokens = (uint32_t)tokens;
     uint32_t threads;
     int nv;
-    shape(cols, &threads, &nv);
+    shape(tokens, cols, &threads, &nv);
     RowFn fn = gate->dtype == EQ_DTYPE_F32 ? pick_out<SILU, true, 0>(out->dtype, nv)
                                            : pick_out<SILU, false, 0>(out->dtype, nv);
     return launch_rows(fn, a, tokens, threads, stream);

@@ -356,36 +356,28 @@ def _stream_of(stream, t) -> int | None:
 def _matrix(name: str, t, tokens: int, cols: int, scale=None) -> bytes:
     """eq_matrix of a [tokens, cols] tensor (or [cols] for one token) whose last
     dimension is dense."""
+    dtype = _activation_types().get(t.dtype, 0)
     shape, stride = t.shape, t.stride()
-    if len(shape) == 2:
-        rows, ld = shape[0], stride[0]
-    elif len(shape) == 1:
-        rows, ld = 1, shape[0]
-    else:
-        raise ValueError(f"{name}: one or two dimensions, got shape {tuple(shape)}")
-    if rows != tokens or shape[-1] != cols:
+    two = len(shape) == 2
+    if not (two or len(shape) == 1) or (shape[0] if two else 1) != tokens or shape[-1] != cols:
         raise ValueError(f"{name}: expected [{tokens}, {cols}], got {tuple(shape)}")
     if stride[-1] != 1 and cols > 1:
         raise ValueError(f"{name}: elements of a row must be contiguous")
-    if rows <= 1 or cols == 1 and ld < 1:
-        ld = max(ld, cols)
-    dtype = _activation_types().get(t.dtype)
-    if dtype is None:
-        raise ValueError(f"{name}: type {t.dtype} is not supported")
-    d_scale = 0
-    if dtype == EQ_DTYPE_INT8 or dtype == EQ_DTYPE_E4M3:
-        if scale is None:
-            raise ValueError(f"{name}: an 8-bit matrix needs its scales (fp32, one per row)")
-        if scale.dtype != _torch().float32 or scale.numel() != tokens or not scale.is_contiguous():
-            raise ValueError(f"{name}: scales must be {tokens} contiguous fp32 values")
-        if not scale.is_cuda:
-            raise ValueError(f"{name}: scales must be on the GPU")
-        d_scale = scale.data_ptr()
-    elif scale is not None:
-        raise ValueError(f"{name}: scales belong to 8-bit types")
     if not t.is_cuda:
         raise ValueError(f"{name}: must be on the GPU")
-    return _pack_matrix(t.data_ptr(), ld, d_scale, dtype, 0)
+    # one row has any stride
+    ld = stride[0] if two and tokens > 1 else cols
+    if dtype == EQ_DTYPE_F32 or dtype == EQ_DTYPE_BF16:
+        if scale is not None:
+            raise ValueError(f"{name}: scales belong to 8-bit types")
+        return _pack_matrix(t.data_ptr(), ld, 0, dtype, 0)
+    if dtype == 0:
+        raise ValueError(f"{name}: type {t.dtype} is not supported")
+    if scale is None:
+        raise ValueError(f"{name}: an 8-bit matrix needs its scales (fp32, one per row)")
+    if scale.dtype != _torch().float32 or scale.numel() != tokens or not scale.is_contiguous() or not scale.is_cuda:
+        raise ValueError(f"{name}: scales must be {tokens} contiguous fp32 values on the GPU")
+    return _pack_matrix(t.data_ptr(), ld, scale.data_ptr(), dtype, 0)
 
 
 def _size(t) -> tuple[int, int]:
