@@ -635,25 +635,40 @@ W4Fn pick(uint32_t w, uint32_t x, bool z, uint32_t group, uint32_t nt, uint32_t 
              : pick_group<EQ_DTYPE_INT4, EQ_DTYPE_INT8, false>(group, nt, tp, r, wide);
 }
 
-// Row-major codes, scales and zeros to tiles: one thread per 4-byte word of
-// codes; the first 16 * (groups per tile) threads of a tile also place its
+// Row-major codes, scales and zeros to tiles: a workgroup per tile, a thread
+// per word, reading its 8 columns as they lie (one u32 where rows are 4-byte
+// aligned); the first 16 * (groups per tile) threads also place the tile's
 // scales and zeros.
 __global__ void __launch_bounds__(256)
 k_w4_pack(W4Args t, uint32_t e2m1, const uint8_t *__restrict__ src, const uint16_t *__restrict__ src_scales,
-          const uint8_t *__restrict__ src_zeros, u32x4 *codes, uint16_t *scales, uint8_t *zeros) {
-    const uint32_t k_tiles = (t.cols + kTileCols - 1) / kTileCols;
+          const uint8_t *__restrict__ src_zeros, uint32_t *codes, uint16_t *scales, uint8_t *zeros) {
+    const uint32_t k_tiles = t.k_tiles;
     const uint64_t tile = blockIdx.x;
     const uint32_t row_tile = (uint32_t)(tile / k_tiles), kt = (uint32_t)(tile % k_tiles);
     const uint64_t pitch = (t.cols + 1ull) / 2;
-    const uint32_t lane = threadIdx.x >> 2, j = threadIdx.x & 3u;
-    const uint32_t row = row_tile * kTileRows + (lane & 15u);
-    const uint32_t k = kt * kTileCols + word_col(t.group, lane >> 4, j);
+    const uint32_t i = threadIdx.x & 15u, r16 = threadIdx.x >> 4;  // columns 8 i .. 8 i + 7 of row r16
+    const uint32_t row = row_tile * kTileRows + r16, c0 = kt * kTileCols + i * 8;
+    const bool words = ((reinterpret_cast<uintptr_t>(src) | pitch) & 3u) == 0;
     uint32_t w = 0;
-    for (uint32_t p = 0; p < 8; ++p) {
-        const uint32_t c = k + (e2m1 ? p : p < 4 ? 2 * p : 2 * p - 7);
-        if (row < t.rows && c < t.cols) w |= (uint32_t)((src[row * pitch + c / 2] >> (4 * (c & 1))) & 15u) << (4 * p);
+    if (row < t.rows) {
+        const uint8_t *p = src + row * pitch + c0 / 2;
+        if (words && c0 + 8 <= t.cols) {
+            w = *reinterpret_cast<const uint32_t *>(p);
+        } else {
+            for (uint32_t k = 0; k < 8; ++k)
+                if (c0 + k < t.cols) w |= (uint32_t)((p[k / 2] >> (4 * (k & 1))) & 15u) << (4 * k);
+        }
     }
-    reinterpret_cast<uint32_t *>(codes)[tile * 256 + threadIdx.x] = w;
+    if (!e2m1) {  // 0 1 2 3 4 5 6 7 -> 0 2 4 6 1 3 5 7
+        uint32_t even = w & 0x0F0F0F0Fu, odd = (w >> 4) & 0x0F0F0F0Fu;
+        even = (even | even >> 4) & 0x00FF00FFu;
+        odd = (odd | odd >> 4) & 0x00FF00FFu;
+        w = ((even | even >> 8) & 0xFFFFu) | (odd | odd >> 8) << 16;
+    }
+    // the word's place: word_col turned round
+    const uint32_t quarter = t.group == 32 ? i & 3u : i >> 1 & 3u;
+    const uint32_t j = t.group == 32 ? i >> 2 : i >> 3 << 1 | (i & 1u);
+    codes[tile * 256 + (quarter * 16 + r16) * 4 + j] = w;
     const uint32_t per_tile = kTileCols / t.group;
     if (threadIdx.x < 16 * per_tile) {
         const uint32_t r = row_tile * kTileRows + threadIdx.x / per_tile;
@@ -738,7 +753,7 @@ eq_status eq_w4_pack(const eq_w4_tensor *t, const uint8_t *d_codes, const uint16
     if (n > kMaxThreads / 256) return EQ_EINVAL;
     hipLaunchKernelGGL(k_w4_pack, dim3((uint32_t)n), dim3(256), 0, static_cast<hipStream_t>(stream), tensor_args(*t),
                        t->dtype == EQ_DTYPE_E2M1 ? 1u : 0u, d_codes, d_scales, d_zeros,
-                       static_cast<u32x4 *>(t->d_codes), t->d_scales, t->d_zeros);
+                       static_cast<uint32_t *>(t->d_codes), t->d_scales, t->d_zeros);
     return hipGetLastError() == hipSuccess ? EQ_OK : EQ_EHIP;
 }
 
