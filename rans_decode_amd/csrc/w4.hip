@@ -299,7 +299,8 @@ __device__ __forceinline__ void store_y(const W4Args &T, bool f32, uint32_t t, u
 // wave, so a lane keeps the sums of piece (4 quarter) / TP and scales them by
 // that piece's group; the pieces are added up in the epilogue. NT > 1 (TP =
 // 16): up to 16 * NT tokens.
-template <uint32_t W, uint32_t X, uint32_t S, bool Z, int TP, int NT, int R, int D>
+// NI: registers of a sum that hold wanted tokens (4, or 1 for a single token).
+template <uint32_t W, uint32_t X, uint32_t S, bool Z, int TP, int NT, int R, int D, int NI = 4>
 __global__ void __launch_bounds__(64 * kWaves) k_w4(W4Launch a) {
     typedef Kind<W, X, S, Z> K;
     constexpr uint32_t XB = X == EQ_DTYPE_BF16 ? 2 : 1;
@@ -384,7 +385,7 @@ __global__ void __launch_bounds__(64 * kWaves) k_w4(W4Launch a) {
                 const float s = st.w.scale(r, g) * K::kScale, zero = st.w.zero(r, g);
 #pragma unroll
                 for (int n = 0; n < NT; ++n)
-                    for (int i = 0; i < 4; ++i) {
+                    for (int i = 0; i < NI; ++i) {
                         auto v = d[n][r][0][i];
                         if constexpr (LJ == 2) v = my_piece ? d[n][r][1][i] : v;
                         if constexpr (LJ == 4) {
@@ -441,7 +442,7 @@ __global__ void __launch_bounds__(64 * kWaves) k_w4(W4Launch a) {
             for (uint32_t w = 0; w < kw_n; ++w)
                 for (uint32_t jj = 0; jj < LJ; ++jj) s += part[orw * kw_n + w][r][lane + jj * 4 * TP];
             const uint32_t row = (t0 + r) * kTileRows + i16;
-            for (int i = 0; i < 4; ++i) {
+            for (int i = 0; i < NI; ++i) {
                 const uint32_t t = token0 + n * 16 + quarter * 4 + i;
                 if (t < a.tokens && row < T.rows) {
                     float v = s[i];
@@ -609,8 +610,10 @@ W4Fn pick_shape(uint32_t nt, uint32_t tp, uint32_t r, bool wide) {
         if (nt == 2) return r == 1 ? k_w4_wide<W, X, S, Z, 2, 1> : k_w4_wide<W, X, S, Z, 2, 2>;
         return r == 1 ? k_w4_wide<W, X, S, Z, 4, 1> : k_w4_wide<W, X, S, Z, 4, 2>;
     }
-    if (tp == 4) {
-        if constexpr (Kind<W, X, S, Z>::Q == 4) return k_w4<W, X, S, Z, 4, 1, 1, 4>;
+    if (tp <= 4) {
+        if constexpr (Kind<W, X, S, Z>::Q == 4)
+            return tp == 1 ? k_w4<W, X, S, Z, 4, 1, 1, 4, 1> : k_w4<W, X, S, Z, 4, 1, 1, 4>;
+        if (tp == 1) return k_w4<W, X, S, Z, 8, 1, 1, 4, 1>;
         tp = 8;
     }
     if (tp == 8) return r == 1 ? k_w4<W, X, S, Z, 8, 1, 1, 4> : k_w4<W, X, S, Z, 8, 1, 2, 2>;
@@ -699,7 +702,7 @@ bool tensor_ok(const eq_w4_tensor &t) {
 }
 
 struct Shape {
-    uint32_t nt, tp, r;  // token tiles of tp (4, 8 or 16) tokens and rows of tiles per wave
+    uint32_t nt, tp, r;  // token tiles of tp (1, 4, 8 or 16) tokens and rows of tiles per wave
     bool wide;           // k_w4_wide
 };
 
@@ -710,7 +713,7 @@ Shape shape(uint64_t tokens, uint64_t row_tiles, uint64_t fewest) {
     while (r > 1 && (row_tiles < 128 * r || fewest < r)) r /= 2;
     const bool wide = tokens > 8 && row_tiles >= (nt == 1 ? 1536 : nt == 2 ? 1024 : 640) && fewest >= 2;
     if (wide) r = row_tiles >= 2560 ? 2 : 1;
-    return {nt, tokens <= 4 ? 4u : tokens <= 8 ? 8u : 16u, r, wide};
+    return {nt, tokens == 1 ? 1u : tokens <= 4 ? 4u : tokens <= 8 ? 8u : 16u, r, wide};
 }
 
 // Waves that share out the columns (log2): as many as have two tiles each.
