@@ -290,17 +290,22 @@ __device__ __forceinline__ void store_y(const W4Args &T, bool f32, uint32_t t, u
 // their way while it computes, and the k_waves partial sums are joined in LDS
 // in wave order.
 //
-// TP tokens share a matrix instruction's 16 rows of A: with TP < 16 row m
-// holds token m % TP and piece m / TP of every 16 / TP pieces, so that one
-// load brings several pieces and few tokens cost few loads (one token of bf16
-// took 4 loads a tile, each as large as the codes' own, and bounded the
-// kernel). Every piece's instruction then computes all rows, of which those of
-// its own piece are kept: rows 4 quarter + i are registers i of a quarter
-// wave, so a lane keeps the sums of piece (4 quarter) / TP and scales them by
-// that piece's group; the pieces are added up in the epilogue. NT > 1 (TP =
-// 16): up to 16 * NT tokens.
-// NI: registers of a sum that hold wanted tokens (4, or 1 for a single token).
-template <uint32_t W, uint32_t X, uint32_t S, bool Z, int TP, int NT, int R, int D, int NI = 4>
+// TP tokens share a matrix instruction's 16 rows of A: with TP < 16 row
+// m = LJ t + jj holds token t and piece jj of every LJ = 16 / TP pieces, so that
+// one load brings several pieces and few tokens cost few loads (one token of
+// bf16 took 4 loads a tile, each as large as the codes' own, and bounded the
+// kernel). Every piece's instruction then computes all rows; those of its own
+// piece are, with rows 4 quarter + i in registers i of a quarter wave, the
+// registers i = jj mod LJ, which alone are scaled and added up. TP = 4 keeps one
+// token per lane, TP = 8 two, TP = 16 four. NT > 1 (TP = 16): up to 16 * NT
+// tokens.
+//
+// TP = 16: a load whose neighbouring lanes read 16 different rows takes the
+// cache 64 look-ups, one whose 4 neighbours read 64 consecutive bytes 16; so
+// lanes load in that order, lane = 4 row + quarter, and swap through LDS (a
+// wave's own slots: no barrier). The slots are rotated so that neither side
+// meets bank conflicts.
+template <uint32_t W, uint32_t X, uint32_t S, bool Z, int TP, int NT, int R, int D>
 __global__ void __launch_bounds__(64 * kWaves) k_w4(W4Launch a) {
     typedef Kind<W, X, S, Z> K;
     constexpr uint32_t XB = X == EQ_DTYPE_BF16 ? 2 : 1;
@@ -308,10 +313,16 @@ __global__ void __launch_bounds__(64 * kWaves) k_w4(W4Launch a) {
     constexpr uint32_t NL = K::Q / LJ;                    // loads per tile
     constexpr uint32_t F = K::PG > LJ ? K::PG / LJ : 1;   // loads that share a lane's group
     static_assert(NL >= 1 && NL % F == 0 && (NT == 1 || TP == 16), "tokens, pieces and groups fit");
-    __shared__ f32x4 part[kWaves][R][64];
+    constexpr uint32_t NI = 4 / LJ;                       // tokens a lane keeps sums of, per token tile
+    typedef float Acc __attribute__((ext_vector_type(NI)));
+    __shared__ Acc part[kWaves][R][64];
+    __shared__ typename K::Raw swap[TP == 16 ? kWaves : 1][TP == 16 ? NL : 1][64];
     const uint32_t wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), lane = threadIdx.x & 63u;
     const uint32_t i16 = lane & 15u, quarter = lane >> 4;
-    const uint32_t my_piece = 4 * quarter / TP;  // of a load's LJ, the one whose sums this lane keeps
+    // where this lane's loads come from, and its slots for swapping them
+    const uint32_t load_row = TP == 16 ? lane >> 2 : i16, load_quarter = TP == 16 ? lane & 3u : quarter;
+    const uint32_t put = load_quarter * 16 + ((load_row + 4 * load_quarter) & 15u);
+    const uint32_t get = quarter * 16 + ((i16 + 4 * quarter) & 15u);
     const uint32_t ti = tensor_of(a, blockIdx.x);
     const W4Args &T = a.t[ti];
     const uint32_t kw_n = 1u << T.kw_log2, rw_n = kWaves >> T.kw_log2;
@@ -323,12 +334,12 @@ __global__ void __launch_bounds__(64 * kWaves) k_w4(W4Launch a) {
     const char *x_row[NT];
     for (int n = 0; n < NT; ++n) {
         // token rows past the end repeat the last one; their sums are not stored
-        uint32_t t = token0 + n * 16 + i16 % TP;
+        uint32_t t = token0 + n * 16 + load_row / LJ;
         t = t < a.tokens ? t : a.tokens - 1;
         x_row[n] = static_cast<const char *>(T.x) + (uint64_t)t * T.ldx * XB;
     }
     uint32_t x_col[NL];
-    for (uint32_t l = 0; l < NL; ++l) x_col[l] = K::col(quarter, l * LJ + i16 / TP);
+    for (uint32_t l = 0; l < NL; ++l) x_col[l] = K::col(load_quarter, l * LJ + load_row % LJ);
     // rows of tiles past the end: the wave computes its R rows from the last
     // R that exist (R <= row_tiles, see the launcher), stores skip them
     uint32_t tile0 = wg_tile + rw * R;
@@ -356,7 +367,7 @@ __global__ void __launch_bounds__(64 * kWaves) k_w4(W4Launch a) {
             }
     };
 
-    f32x4 acc[NT][R] = {};
+    Acc acc[NT][R] = {};
     auto compute = [&](const St &st) {
 #pragma unroll
         for (uint32_t f = 0; f < NL / F; ++f) {
@@ -366,7 +377,12 @@ __global__ void __launch_bounds__(64 * kWaves) k_w4(W4Launch a) {
                 typename K::Op xa[NT];
 #pragma unroll
                 for (int n = 0; n < NT; ++n) {
-                    xa[n] = K::acts(st.x[n][l]);
+                    if constexpr (TP == 16) {
+                        swap[wave][l][put] = st.x[n][l];
+                        xa[n] = K::acts(swap[wave][l][get]);
+                    } else {
+                        xa[n] = K::acts(st.x[n][l]);
+                    }
                     if constexpr (K::kSumX) sx[n] = K::mma(xa[n], K::ones(), sx[n]);
                 }
 #pragma unroll
@@ -378,23 +394,19 @@ __global__ void __launch_bounds__(64 * kWaves) k_w4(W4Launch a) {
                         for (int n = 0; n < NT; ++n) d[n][r][jj] = K::mma(xa[n], b, d[n][r][jj]);
                     }
             }
-            // the lane's group: the same for all lanes, or by its piece
-            const uint32_t g = (f * F * LJ + (LJ > K::PG ? my_piece : 0)) / K::PG;
 #pragma unroll
-            for (int r = 0; r < R; ++r) {
-                const float s = st.w.scale(r, g) * K::kScale, zero = st.w.zero(r, g);
+            for (uint32_t jj = 0; jj < LJ; ++jj) {
+                const uint32_t g = (f * F * LJ + jj) / K::PG;  // the group of this piece (of all F loads)
 #pragma unroll
-                for (int n = 0; n < NT; ++n)
-                    for (int i = 0; i < NI; ++i) {
-                        auto v = d[n][r][0][i];
-                        if constexpr (LJ == 2) v = my_piece ? d[n][r][1][i] : v;
-                        if constexpr (LJ == 4) {
-                            v = my_piece == 1 ? d[n][r][1 % LJ][i] : v;
-                            v = my_piece == 2 ? d[n][r][2 % LJ][i] : v;
-                            v = my_piece == 3 ? d[n][r][3 % LJ][i] : v;
+                for (int r = 0; r < R; ++r) {
+                    const float s = st.w.scale(r, g) * K::kScale, zero = st.w.zero(r, g);
+#pragma unroll
+                    for (int n = 0; n < NT; ++n)
+                        for (uint32_t i = 0; i < NI; ++i) {
+                            const uint32_t at = i * LJ + jj;
+                            acc[n][r][i] = fmaf(s, K::value(d[n][r][jj][at], sx[n][at], zero), acc[n][r][i]);
                         }
-                        acc[n][r][i] = fmaf(s, K::value(v, sx[n][i], zero), acc[n][r][i]);
-                    }
+                }
             }
         }
     };
@@ -437,13 +449,11 @@ __global__ void __launch_bounds__(64 * kWaves) k_w4(W4Launch a) {
             const bool moved = t0 + R > row_tiles;
             if (moved && (t0 >= row_tiles || row_tiles - R + r < t0)) continue;  // another wave's row of tiles
             if (moved) t0 = row_tiles - R;
-            if (4 * quarter >= TP) continue;  // lanes of the first piece add up the others'
-            f32x4 s = {};
-            for (uint32_t w = 0; w < kw_n; ++w)
-                for (uint32_t jj = 0; jj < LJ; ++jj) s += part[orw * kw_n + w][r][lane + jj * 4 * TP];
+            Acc s = {};
+            for (uint32_t w = 0; w < kw_n; ++w) s += part[orw * kw_n + w][r][lane];
             const uint32_t row = (t0 + r) * kTileRows + i16;
-            for (int i = 0; i < NI; ++i) {
-                const uint32_t t = token0 + n * 16 + quarter * 4 + i;
+            for (uint32_t i = 0; i < NI; ++i) {
+                const uint32_t t = token0 + n * 16 + quarter * NI + i;
                 if (t < a.tokens && row < T.rows) {
                     float v = s[i];
                     if constexpr (X != EQ_DTYPE_BF16) v *= T.x_scale[t];
@@ -472,7 +482,12 @@ __global__ void __launch_bounds__(64 * kWaves) k_w4_wide(W4Launch a) {
     constexpr uint32_t kOps = K::Q / KS::Q;            // operands from one load (1, or 2 for E4M3 x 64)
     constexpr uint32_t kLoads = C * NT * KS::Q / kWaves;  // a wave's loads for a chunk
     static_assert(kLoads >= 1 && C * NT * KS::Q % kWaves == 0, "waves share out a chunk's loads evenly");
+    // sum(x) of every token and group, by the wave that stages it (where one
+    // wave stages whole token tiles); one matrix instruction per piece and wave
+    // otherwise
+    constexpr bool kSums = K::kSumX && kLoads % KS::Q == 0;
     __shared__ typename K::Op xs[2][C][NT][K::Q][64];
+    __shared__ typename K::Sum xsum[2][C][NT][P][kSums ? 4 : 1];
     const uint32_t wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), lane = threadIdx.x & 63u;
     const uint32_t i16 = lane & 15u, quarter = lane >> 4;
     const uint32_t ti = tensor_of(a, blockIdx.x);
@@ -484,14 +499,19 @@ __global__ void __launch_bounds__(64 * kWaves) k_w4_wide(W4Launch a) {
     const uint32_t tile0 = want + R <= row_tiles ? want : row_tiles - R;
     const uint64_t base = (uint64_t)tile0 * k_tiles;
 
-    // the wave's loads of a chunk: (tile, token tile, piece) triples
+    // the wave's loads of a chunk: (tile, token tile, piece) triples, in the
+    // lane order of k_w4's TP = 16 (not where the sums are taken from the
+    // registers, which want operand order); operands lie in its slots
+    const uint32_t load_row = kSums ? i16 : lane >> 2, load_quarter = kSums ? quarter : lane & 3u;
+    const uint32_t put = load_quarter * 16 + ((load_row + 4 * load_quarter) & 15u);
+    const uint32_t get = quarter * 16 + ((i16 + 4 * quarter) & 15u);
     const char *x_at[kLoads];
     uint32_t x_col[kLoads], x_to[kLoads];
     for (uint32_t i = 0; i < kLoads; ++i) {
         const uint32_t k = wave * kLoads + i, p = k % KS::Q, n = k / KS::Q % NT, tile = k / KS::Q / NT;
-        uint32_t t = token0 + n * 16 + i16;
+        uint32_t t = token0 + n * 16 + load_row;
         t = t < a.tokens ? t : a.tokens - 1;
-        x_col[i] = tile * kTileCols + KS::col(quarter, p);
+        x_col[i] = tile * kTileCols + KS::col(load_quarter, p);
         x_at[i] = static_cast<const char *>(T.x) + ((uint64_t)t * T.ldx + x_col[i]) * XB;
         x_to[i] = (tile * NT + n) * K::Q + p * kOps;
     }
@@ -502,13 +522,20 @@ __global__ void __launch_bounds__(64 * kWaves) k_w4_wide(W4Launch a) {
     };
     auto put_x = [&](uint32_t buf) {
         typename K::Op(*to)[64] = &xs[buf][0][0][0];
+        [[maybe_unused]] typename K::Sum sx = {};
+#pragma unroll
         for (uint32_t i = 0; i < kLoads; ++i) {
             const auto o = KS::acts(raw[i]);
             if constexpr (kOps == 2) {
-                to[x_to[i]][lane] = o.h[0];
-                to[x_to[i] + 1][lane] = o.h[1];
+                to[x_to[i]][put] = o.h[0];
+                to[x_to[i] + 1][put] = o.h[1];
             } else {
-                to[x_to[i]][lane] = o;
+                to[x_to[i]][put] = o;
+                if constexpr (kSums) {
+                    sx = i % K::PG ? K::mma(o, K::ones(), sx) : K::mma(o, K::ones(), typename K::Sum{});
+                    // every column of the result is the sums; column 0 stores them
+                    if (i % K::PG == K::PG - 1 && i16 == 0) (&xsum[buf][0][0][0][0])[(x_to[i] / K::PG) * 4 + quarter] = sx;
+                }
             }
         }
     };
@@ -519,9 +546,10 @@ __global__ void __launch_bounds__(64 * kWaves) k_w4_wide(W4Launch a) {
         for (uint32_t g = 0; g < P; ++g) {
             typename K::Op b[K::PG][R], xa[2][K::PG];
             float s[R], zero[R];
+            [[maybe_unused]] typename K::Sum sn[3];
             auto fetch = [&](int n) {
-                for (uint32_t p = 0; p < K::PG; ++p) xa[n & 1][p] = xs[buf][tile][n][g * K::PG + p][lane];
-                __builtin_amdgcn_sched_barrier(0);
+                for (uint32_t p = 0; p < K::PG; ++p) xa[n & 1][p] = xs[buf][tile][n][g * K::PG + p][get];
+                if constexpr (kSums) sn[n % 3] = xsum[buf][tile][n][g][quarter];
             };
             fetch(0);
 #pragma unroll
@@ -537,9 +565,10 @@ __global__ void __launch_bounds__(64 * kWaves) k_w4_wide(W4Launch a) {
                 if (n + 1 < NT) fetch(n + 1);
                 if (n < NT) {
                     sx[n & 1] = typename K::Sum{};
+                    if constexpr (kSums) sx[n & 1] = sn[n % 3];
                     for (int r = 0; r < R; ++r) d[n & 1][r] = typename K::Sum{};
                     for (uint32_t p = 0; p < K::PG; ++p) {
-                        if constexpr (K::kSumX) sx[n & 1] = K::mma(xa[n & 1][p], K::ones(), sx[n & 1]);
+                        if constexpr (K::kSumX && !kSums) sx[n & 1] = K::mma(xa[n & 1][p], K::ones(), sx[n & 1]);
                         for (int r = 0; r < R; ++r) d[n & 1][r] = K::mma(xa[n & 1][p], b[p][r], d[n & 1][r]);
                     }
                 }
@@ -571,6 +600,8 @@ __global__ void __launch_bounds__(64 * kWaves) k_w4_wide(W4Launch a) {
 #pragma unroll
         for (uint32_t d = 0; d < C; ++d) {
             compute(w[d], ch & 1, d);
+            for (int n = 0; n < NT; ++n)
+                for (int r = 0; r < R; ++r) asm volatile("" : "+v"(acc[n][r]));
             __builtin_amdgcn_sched_barrier(0);
             load_w(w[d], (ch + 1) * C + d);
             __builtin_amdgcn_sched_barrier(0);
@@ -610,15 +641,13 @@ W4Fn pick_shape(uint32_t nt, uint32_t tp, uint32_t r, bool wide) {
         if (nt == 2) return r == 1 ? k_w4_wide<W, X, S, Z, 2, 1> : k_w4_wide<W, X, S, Z, 2, 2>;
         return r == 1 ? k_w4_wide<W, X, S, Z, 4, 1> : k_w4_wide<W, X, S, Z, 4, 2>;
     }
-    if (tp <= 4) {
-        if constexpr (Kind<W, X, S, Z>::Q == 4)
-            return tp == 1 ? k_w4<W, X, S, Z, 4, 1, 1, 4, 1> : k_w4<W, X, S, Z, 4, 1, 1, 4>;
-        if (tp == 1) return k_w4<W, X, S, Z, 8, 1, 1, 4, 1>;
+    if (tp == 4) {
+        if constexpr (Kind<W, X, S, Z>::Q == 4) return k_w4<W, X, S, Z, 4, 1, 1, 4>;
         tp = 8;
     }
     if (tp == 8) return r == 1 ? k_w4<W, X, S, Z, 8, 1, 1, 4> : k_w4<W, X, S, Z, 8, 1, 2, 2>;
-    if (nt == 1) return r == 1 ? k_w4<W, X, S, Z, 16, 1, 1, 2> : k_w4<W, X, S, Z, 16, 1, 2, 2>;
-    if (nt == 2) return r == 1 ? k_w4<W, X, S, Z, 16, 2, 1, 2> : k_w4<W, X, S, Z, 16, 2, 2, 2>;
+    if (nt == 1) return r == 1 ? k_w4<W, X, S, Z, 16, 1, 1, 2> : r == 2 ? k_w4<W, X, S, Z, 16, 1, 2, 2> : k_w4<W, X, S, Z, 16, 1, 4, 2>;
+    if (nt == 2) return r == 1 ? k_w4<W, X, S, Z, 16, 2, 1, 2> : r == 2 ? k_w4<W, X, S, Z, 16, 2, 2, 2> : k_w4<W, X, S, Z, 16, 2, 4, 2>;
     return r == 1 ? k_w4<W, X, S, Z, 16, 4, 1, 2> : k_w4<W, X, S, Z, 16, 4, 2, 2>;
 }
 template <uint32_t W, uint32_t X, bool Z>
@@ -702,18 +731,18 @@ bool tensor_ok(const eq_w4_tensor &t) {
 }
 
 struct Shape {
-    uint32_t nt, tp, r;  // token tiles of tp (1, 4, 8 or 16) tokens and rows of tiles per wave
+    uint32_t nt, tp, r;  // token tiles of tp (4, 8 or 16) tokens and rows of tiles per wave
     bool wide;           // k_w4_wide
 };
 
 // R: rows of tiles that share a wave's activations.
 Shape shape(uint64_t tokens, uint64_t row_tiles, uint64_t fewest) {
     const uint32_t nt = tokens <= 16 ? 1 : tokens <= 32 ? 2 : 4;
-    uint32_t r = tokens > 4 ? 2 : 1;
+    uint32_t r = tokens <= 4 ? 1 : tokens <= 8 || nt == 4 || row_tiles < 640 ? 2 : 4;
     while (r > 1 && (row_tiles < 128 * r || fewest < r)) r /= 2;
     const bool wide = tokens > 8 && row_tiles >= (nt == 1 ? 1536 : nt == 2 ? 1024 : 640) && fewest >= 2;
     if (wide) r = row_tiles >= 2560 ? 2 : 1;
-    return {nt, tokens == 1 ? 1u : tokens <= 4 ? 4u : tokens <= 8 ? 8u : 16u, r, wide};
+    return {nt, tokens <= 4 ? 4u : tokens <= 8 ? 8u : 16u, r, wide};
 }
 
 // Waves that share out the columns (log2): as many as have two tiles each.
