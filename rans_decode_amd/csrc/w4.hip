@@ -285,6 +285,13 @@ __device__ __forceinline__ void store_y(const W4Args &T, bool f32, uint32_t t, u
     else static_cast<uint16_t *>(T.y)[t * T.ldy + row] = (uint16_t)pack_bf16(v, 0.0f);
 }
 
+// A wave's LDS accesses are performed in program order; this keeps the compiler
+// from changing that order where lanes exchange values.
+__device__ __forceinline__ void wave_order() {
+    __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront", "local");
+    __builtin_amdgcn_wave_barrier();
+}
+
 // A workgroup's 8 waves are (8 / k_waves) x k_waves: wave (rw, kw) owns R rows
 // of tiles and every k_waves-th column of tiles; D columns of its data are on
 // their way while it computes, and the k_waves partial sums are joined in LDS
@@ -379,7 +386,9 @@ __global__ void __launch_bounds__(64 * kWaves) k_w4(W4Launch a) {
                 for (int n = 0; n < NT; ++n) {
                     if constexpr (TP == 16) {
                         swap[wave][l][put] = st.x[n][l];
+                        wave_order();
                         xa[n] = K::acts(swap[wave][l][get]);
+                        wave_order();
                     } else {
                         xa[n] = K::acts(st.x[n][l]);
                     }
@@ -637,13 +646,13 @@ typedef void (*W4Fn)(W4Launch);
 template <uint32_t W, uint32_t X, bool Z, uint32_t S>
 W4Fn pick_shape(uint32_t nt, uint32_t tp, uint32_t r, bool wide) {
     if (wide) {
-        if (nt == 1) return r == 1 ? k_w4_wide<W, X, S, Z, 1, 1> : k_w4_wide<W, X, S, Z, 1, 2>;
+        if (nt == 1) return k_w4_wide<W, X, S, Z, 1, 2>;
         if (nt == 2) return r == 1 ? k_w4_wide<W, X, S, Z, 2, 1> : k_w4_wide<W, X, S, Z, 2, 2>;
         return r == 1 ? k_w4_wide<W, X, S, Z, 4, 1> : k_w4_wide<W, X, S, Z, 4, 2>;
     }
     if (tp == 4) {
-        if constexpr (Kind<W, X, S, Z>::Q == 4) return k_w4<W, X, S, Z, 4, 1, 1, 4>;
-        tp = 8;
+        if constexpr (Kind<W, X, S, Z>::Q == 4) return r == 1 ? k_w4<W, X, S, Z, 4, 1, 1, 4> : k_w4<W, X, S, Z, 4, 1, 2, 2>;
+        tp = 8;  // 64 columns a piece: two pieces a load
     }
     if (tp == 8) return r == 1 ? k_w4<W, X, S, Z, 8, 1, 1, 4> : k_w4<W, X, S, Z, 8, 1, 2, 2>;
     if (nt == 1) return r == 1 ? k_w4<W, X, S, Z, 16, 1, 1, 2> : r == 2 ? k_w4<W, X, S, Z, 16, 1, 2, 2> : k_w4<W, X, S, Z, 16, 1, 4, 2>;
@@ -735,14 +744,27 @@ struct Shape {
     bool wide;           // k_w4_wide
 };
 
-// R: rows of tiles that share a wave's activations.
+// Measured on MI355X (graph replays, us; rows of tiles of 16 rows):
+//  * rows of tiles a wave takes (r), whose activations are loaded once: one
+//    token 1 (its activations are small: 4096 x 4096 3.6, with two 5.5); 2 to 8
+//    tokens 2 (gate + up 57344 x 8192, four tokens bf16 41.3, one 47.0; eight
+//    tokens 46.9, one 62.0); 9 to 32 tokens 4 where 160 workgroups remain
+//    (11008 x 4096, 16 tokens bf16 9.7, two 12.3) and 2 below (8192 x 28672
+//    E4M3 26.5, four 37.1); 33 to 64 tokens 2 (registers). Halved while fewer
+//    than 128 workgroups would remain.
+//  * k_w4_wide where its workgroups of 8 r rows of tiles still fill the chip:
+//    16 tokens from 2560 rows of tiles (3584: bf16 49.1, k_w4 54.5; 1792: int8
+//    28.3, k_w4 25.8), 32 from 1536 (3584: int8 48.0, k_w4 58.6; 1280: 37.4,
+//    36.9), 64 from 1024 (3584: int8 57.5, k_w4 112; 688: bf16 33.0, 29.7);
+//    there r = 2 from 2560 (3584, 64 tokens int8: 62, one 69; 1792: 51, 41).
 Shape shape(uint64_t tokens, uint64_t row_tiles, uint64_t fewest) {
     const uint32_t nt = tokens <= 16 ? 1 : tokens <= 32 ? 2 : 4;
-    uint32_t r = tokens <= 4 ? 1 : tokens <= 8 || nt == 4 || row_tiles < 640 ? 2 : 4;
+    const uint32_t tp = tokens <= 4 ? 4 : tokens <= 8 ? 8 : 16;
+    if (tokens > 8 && fewest >= 2 && row_tiles >= (nt == 1 ? 2560 : nt == 2 ? 1536 : 1024))
+        return {nt, tp, row_tiles >= 2560 ? 2u : 1u, true};
+    uint32_t r = tokens == 1 ? 1 : tokens <= 8 || nt == 4 || row_tiles < 640 ? 2 : 4;
     while (r > 1 && (row_tiles < 128 * r || fewest < r)) r /= 2;
-    const bool wide = tokens > 8 && row_tiles >= (nt == 1 ? 1536 : nt == 2 ? 1024 : 640) && fewest >= 2;
-    if (wide) r = row_tiles >= 2560 ? 2 : 1;
-    return {nt, tokens <= 4 ? 4u : tokens <= 8 ? 8u : 16u, r, wide};
+    return {nt, tp, r, false};
 }
 
 // Waves that share out the columns (log2): as many as have two tiles each.

@@ -151,6 +151,23 @@ def test_many_rows_exact(kind, zeros, xt, group):
 
 
 @pytest.mark.parametrize("kind,zeros,xt", KINDS)
+@pytest.mark.parametrize("group", [32, 64, 128])
+def test_very_many_rows_exact(kind, zeros, xt, group):
+    """The same with two rows of tiles a wave; the last workgroup's waves partly and wholly past the end."""
+    for i, (tokens, cols) in enumerate([(9, 100), (16, 600), (20, 512), (64, 1025)]):
+        run(9700 + 20 * i + group, tokens, [41000, 33], cols, kind, zeros, xt, group)
+
+
+@pytest.mark.parametrize("kind,zeros,xt", KINDS)
+def test_rows_per_wave_exact(kind, zeros, xt):
+    """Row counts where a wave takes 1, 2 or 4 rows of tiles, with rows of tiles left over, and columns split among 1 to 8 waves."""
+    for i, (tokens, rows, cols) in enumerate([(1, 4100, 300), (3, 4100, 2100), (4, 4117, 130), (7, 4133, 1100), (16, 4133, 600),
+                                              (12, 10260, 1300), (24, 10300, 390), (30, 4150, 2050), (50, 4120, 520)]):
+        run(9900 + i, tokens, [rows], cols, kind, zeros, xt, (32, 64, 128)[i % 3])
+    run(9950, 10, [10241, 64], 260, kind, zeros, xt, 64)
+
+
+@pytest.mark.parametrize("kind,zeros,xt", KINDS)
 def test_single_columns(kind, zeros, xt):
     """x with one 1 per token picks single weights: the layout, column by column."""
     cols, rows, group = 200, 21, 64
