@@ -3,7 +3,7 @@ runs it: the entropy-coded output projection, the residual's addition and
 norm, a 4-bit MLP with int8 activations, and the norm that feeds the next
 block's entropy-coded projections.
 
-    python examples/w4_mlp.py [--hidden 1024] [--inner 2816] [--group 128]
+    python examples/w4_mlp.py [--hidden 1024] [--inner 2816] [--group 128] [--steps 50]
 
     attention output (bf16)
       -> eq_decode_gemv_bf16    o projection, weights entropy-coded      fp32
@@ -14,7 +14,8 @@ block's entropy-coded projections.
       -> eq_add_rmsnorm         residual += down; norm                   bf16
 
 Weights are random. The result is compared with the same steps in 64 bits on
-the same quantised weights; what differs is the rounding of the activations.
+the same quantised weights; what differs is the rounding of the activations. With
+--steps N the step is also captured in a HIP graph and timed over N replays.
 """
 import argparse
 import os
@@ -102,6 +103,7 @@ def main(argv=None):
     ap.add_argument("--hidden", type=int, default=1024)
     ap.add_argument("--inner", type=int, default=2816)
     ap.add_argument("--group", type=int, default=128, choices=(32, 64, 128))
+    ap.add_argument("--steps", type=int, default=0, help="time this many graph replays of the step")
     args = ap.parse_args(argv)
     block = Block(args.hidden, args.inner, args.group)
     attention = torch.randn(args.hidden, device="cuda").to(torch.bfloat16)
@@ -113,6 +115,18 @@ def main(argv=None):
     off_residual = float((residual.double() - want_residual).norm() / want_residual.norm())
     print(f"hidden {args.hidden}, inner {args.inner}, group {args.group}: output {off:.2e}, residual {off_residual:.2e} "
           "from the same step in 64 bits (2-norm)")
+    if args.steps > 0:
+        graph = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(graph):
+            block.step(attention, residual)
+        graph.replay()
+        begin, end = torch.cuda.Event(enable_timing=True), torch.cuda.Event(enable_timing=True)
+        begin.record()
+        for _ in range(args.steps):
+            graph.replay()
+        end.record()
+        torch.cuda.synchronize()
+        print(f"{begin.elapsed_time(end) * 1e3 / args.steps:.1f} us per step (6 kernels, one graph)")
     return off, off_residual
 
 
