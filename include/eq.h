@@ -497,8 +497,8 @@ eq_status eq_w4_pack(const eq_w4_tensor *t, const uint8_t *d_codes, const uint16
  *    other token's x; deterministic, but not bit-reproducible against other
  *    summation orders or token counts.
  * Errors: EQ_EINVAL (as eq_w4_pack; a stride below the width, a missing
- *    scale array, an unknown type, more than 64 * 65535 tokens, 2^23 or more
- *    rows of tiles in one launch), EQ_EUNSUPPORTED (INT8 x with E2M1
+ *    scale array, an unknown type, more than 64 * 65535 tokens or 8388592
+ *    rows), EQ_EUNSUPPORTED (INT8 x with E2M1
  *    weights, E4M3 x with INT4 weights), EQ_EHIP. Everything is checked
  *    before anything is enqueued.
  */

@@ -6,6 +6,7 @@ instruction selection; pipeline.hip is the host-side block schedule.
 """
 import os
 import subprocess
+from concurrent.futures import ThreadPoolExecutor
 
 HERE = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(HERE)
@@ -29,23 +30,19 @@ def build_library(verbose: bool = False, out: str = LIB, defines: dict | None = 
                   build_dir: str = BUILD) -> str:
     """Build libeq.so (or a variant with extra -D defines at `out`)."""
     os.makedirs(build_dir, exist_ok=True)
-    host_o = os.path.join(build_dir, "host_codec.o")
-    dev_o = os.path.join(build_dir, "decode.o")
     dflags = [f"-D{k}={v}" for k, v in (defines or {}).items()]
-    _run(["g++", "-O2", "-std=c++17", "-fPIC", "-pthread", "-Wall", "-Wextra",
-          "-c", os.path.join(CSRC, "host_codec.cpp"), "-o", host_o], verbose)
-    enc_o = os.path.join(build_dir, "encode.o")
-    _run(["hipcc", *HIPCC_FLAGS, *dflags, "-c", os.path.join(CSRC, "decode.hip"), "-o", dev_o], verbose)
-    _run(["hipcc", *HIPCC_FLAGS, *dflags, "-c", os.path.join(CSRC, "encode.hip"), "-o", enc_o], verbose)
-    step_os = []
-    for name in ("rownorm", "w4"):
-        step_os.append(os.path.join(build_dir, name + ".o"))
-        _run(["hipcc", *HIPCC_FLAGS, *dflags, "-c", os.path.join(CSRC, name + ".hip"), "-o", step_os[-1]], verbose)
-    pipe_o = os.path.join(build_dir, "pipeline.o")
-    _run(["hipcc", *HIPCC_FLAGS, "-c", os.path.join(CSRC, "pipeline.hip"), "-o", pipe_o], verbose)
+    sources = {"host_codec": ["g++", "-O2", "-std=c++17", "-fPIC", "-pthread", "-Wall", "-Wextra"],
+               "decode": ["hipcc", *HIPCC_FLAGS, *dflags], "encode": ["hipcc", *HIPCC_FLAGS, *dflags],
+               "rownorm": ["hipcc", *HIPCC_FLAGS, *dflags], "w4": ["hipcc", *HIPCC_FLAGS, *dflags],
+               "pipeline": ["hipcc", *HIPCC_FLAGS]}
+    objects = [os.path.join(build_dir, name + ".o") for name in sources]
+    commands = [[*cc, "-c", os.path.join(CSRC, name + (".cpp" if cc[0] == "g++" else ".hip")), "-o", o]
+                for (name, cc), o in zip(sources.items(), objects)]
+    with ThreadPoolExecutor(max_workers=min(4, os.cpu_count() or 1)) as pool:
+        for done in [pool.submit(_run, c, verbose) for c in commands]:
+            done.result()
     tmp = out + ".tmp"
-    _run(["hipcc", "-shared", f"--offload-arch={ARCH}", host_o, dev_o, enc_o, *step_os, pipe_o, "-o", tmp, "-pthread"],
-         verbose)
+    _run(["hipcc", "-shared", f"--offload-arch={ARCH}", *objects, "-o", tmp, "-pthread"], verbose)
     os.replace(tmp, out)
     return out
 

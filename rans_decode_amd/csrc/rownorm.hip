@@ -89,12 +89,17 @@ __device__ __forceinline__ void store8_f32(void *row, uint32_t at, const float (
     *reinterpret_cast<f32x4_a4 *>(p + 4) = f32x4{v[4], v[5], v[6], v[7]};
 }
 
+// The nearest integer, ties to even. The clamp changes no finite value (see
+// codes4); it gives a NaN an integer, which the conversion alone would not.
+__device__ __forceinline__ uint32_t int8_bits(float t) {
+    return (uint32_t)(int32_t)rintf(__builtin_amdgcn_fmed3f(t, -127.0f, 127.0f)) & 255u;
+}
+
 // Four 8-bit codes. |t| <= L * (1 + 2^-23), which rounds to L.
 template <uint32_t OUT>
 __device__ __forceinline__ uint32_t codes4(float t0, float t1, float t2, float t3) {
     if constexpr (OUT == EQ_DTYPE_INT8) {
-        return ((uint32_t)(int32_t)rintf(t0) & 255u) | ((uint32_t)(int32_t)rintf(t1) & 255u) << 8 |
-               ((uint32_t)(int32_t)rintf(t2) & 255u) << 16 | (uint32_t)(int32_t)rintf(t3) << 24;
+        return int8_bits(t0) | int8_bits(t1) << 8 | int8_bits(t2) << 16 | int8_bits(t3) << 24;
     } else {
         const int a = __builtin_amdgcn_cvt_pk_fp8_f32(t0, t1, 0, false);
         return (uint32_t)__builtin_amdgcn_cvt_pk_fp8_f32(t2, t3, a, true);

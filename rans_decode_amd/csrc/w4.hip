@@ -734,6 +734,9 @@ k_w4_pack(W4Args t, uint32_t e2m1, const uint8_t *__restrict__ src, const uint16
 
 constexpr uint64_t kMaxSide = 0x7FFFFFFFull;
 constexpr uint64_t kMaxThreads = 0xFFFFFFFFull;  // of one grid dimension
+// rows of eq_w4_matvec's tensors: EQ_MAX_BLOCK_TENSORS of them stay below
+// kMaxThreads with a workgroup per row of tiles
+constexpr uint64_t kMaxRows = kTileRows * (kMaxThreads / (64 * kWaves) / EQ_MAX_BLOCK_TENSORS);
 
 uint64_t tiles(uint64_t rows, uint64_t cols) {
     return ((rows + kTileRows - 1) / kTileRows) * ((cols + kTileCols - 1) / kTileCols);
@@ -827,7 +830,7 @@ eq_status eq_w4_matvec(const eq_w4_tensor *tensors, uint32_t n_tensors, const eq
     if (!tensors || !x || !y || tokens > 65535ull * kMaxTokens) return EQ_EINVAL;
     for (uint32_t i = 0; i < n_tensors; ++i) {
         const eq_w4_tensor &t = tensors[i];
-        if (!tensor_ok(t) || x[i].reserved || y[i].reserved) return EQ_EINVAL;
+        if (!tensor_ok(t) || t.rows > kMaxRows || x[i].reserved || y[i].reserved) return EQ_EINVAL;
         if (y[i].dtype != EQ_DTYPE_F32 && y[i].dtype != EQ_DTYPE_BF16) return EQ_EINVAL;
         if (x[i].dtype != EQ_DTYPE_BF16 && x[i].dtype != EQ_DTYPE_INT8 && x[i].dtype != EQ_DTYPE_E4M3) return EQ_EINVAL;
         if (x[i].dtype != EQ_DTYPE_BF16 && x[i].dtype != (t.dtype == EQ_DTYPE_INT4 ? EQ_DTYPE_INT8 : EQ_DTYPE_E4M3))
@@ -872,14 +875,12 @@ eq_status eq_w4_matvec(const eq_w4_tensor *tensors, uint32_t n_tensors, const eq
             t.y = y[i].d;
             t.ldx = x[i].stride;
             t.ldy = y[i].stride;
-            if (wgs > kMaxThreads / (64 * kWaves)) return EQ_EINVAL;
             a.wg_begin[k] = (uint32_t)wgs;
             t.kw_log2 = sh.wide ? 0 : kw_log2(t.k_tiles);
             const uint64_t per_wg = (kWaves >> t.kw_log2) * sh.r;
             wgs += (t.row_tiles + per_wg - 1) / per_wg;
         }
         const uint64_t passes = (tokens + kMaxTokens - 1) / kMaxTokens;
-        if (wgs > kMaxThreads / (64 * kWaves)) return EQ_EINVAL;
         a.tokens = (uint32_t)tokens;
         a.y_f32 = y[first].dtype == EQ_DTYPE_F32;
         hipLaunchKernelGGL(pick(tensors[first].dtype, x[first].dtype, tensors[first].d_zeros != nullptr,

@@ -333,11 +333,16 @@ def eq_bf16_from_f32(x, out, stream=None) -> None:
 # ---------------------------------------------------------------------------
 # The steps around the weight products (torch tensors on the GPU)
 # ---------------------------------------------------------------------------
-@functools.lru_cache(maxsize=None)
-def _activation_types() -> dict:
-    torch = _torch()
-    return {torch.float32: EQ_DTYPE_F32, torch.bfloat16: EQ_DTYPE_BF16, torch.int8: EQ_DTYPE_INT8,
-            torch.float8_e4m3fn: EQ_DTYPE_E4M3}
+_types: dict = {}  # torch's types by the library's numbers, filled at the first use of one
+
+
+def _activation_type(dtype) -> int:
+    """EQ_DTYPE_* of a torch type, 0 if it is none of an activation's."""
+    if not _types:
+        torch = _torch()
+        _types.update({torch.float32: EQ_DTYPE_F32, torch.bfloat16: EQ_DTYPE_BF16, torch.int8: EQ_DTYPE_INT8,
+                       torch.float8_e4m3fn: EQ_DTYPE_E4M3})
+    return _types.get(dtype, 0)
 
 
 @functools.lru_cache(maxsize=None)
@@ -356,17 +361,15 @@ def _stream_of(stream, t) -> int | None:
 def _matrix(name: str, t, tokens: int, cols: int, scale=None) -> bytes:
     """eq_matrix of a [tokens, cols] tensor (or [cols] for one token) whose last
     dimension is dense."""
-    dtype = _activation_types().get(t.dtype, 0)
-    shape, stride = t.shape, t.stride()
-    two = len(shape) == 2
-    if not (two or len(shape) == 1) or (shape[0] if two else 1) != tokens or shape[-1] != cols:
-        raise ValueError(f"{name}: expected [{tokens}, {cols}], got {tuple(shape)}")
+    dtype = _types.get(t.dtype) or _activation_type(t.dtype)
+    stride = t.stride()
+    if t.shape != (tokens, cols) and (tokens != 1 or t.shape != (cols,)):
+        raise ValueError(f"{name}: expected [{tokens}, {cols}], got {tuple(t.shape)}")
     if stride[-1] != 1 and cols > 1:
         raise ValueError(f"{name}: elements of a row must be contiguous")
     if not t.is_cuda:
         raise ValueError(f"{name}: must be on the GPU")
-    # one row has any stride
-    ld = stride[0] if two and tokens > 1 else cols
+    ld = stride[0] if tokens > 1 else cols  # one row has any stride
     if dtype == EQ_DTYPE_F32 or dtype == EQ_DTYPE_BF16:
         if scale is not None:
             raise ValueError(f"{name}: scales belong to 8-bit types")
@@ -399,7 +402,7 @@ def eq_add_rmsnorm(x, weight, eps: float, out, out_scale=None, residual=None, re
     elif residual_out is not None:
         raise ValueError("residual_out without a residual")
     if weight is not None:
-        w_type = _activation_types().get(weight.dtype, 0)
+        w_type = _activation_type(weight.dtype)
         if weight.numel() != cols or not weight.is_contiguous() or not weight.is_cuda:
             raise ValueError(f"weight: {cols} contiguous values on the GPU")
         w = weight.data_ptr()

@@ -130,6 +130,28 @@ def test_norm_many_tokens():
     assert between_roundings(o.cpu().double().numpy(), y.cpu().numpy(), 2 * E * np.abs(y.cpu().numpy()))
 
 
+def test_offsets_past_32_bits():
+    """Rows more than 2^32 bytes apart, inputs and outputs, both kernels."""
+    log("case rows far apart")
+    tokens, cols, step = 3, 1003, (1 << 31) + 6
+    def far(dtype):
+        return torch.empty((tokens - 1) * step + cols, dtype=dtype, device="cuda").as_strided((tokens, cols), (step, 1))
+    near = rows_of(4, tokens, cols, BF16)
+    x, r, ro, o, o8 = far(BF16), far(BF16), far(BF16), far(BF16), far(I8)
+    x.copy_(near)
+    r.copy_(near)
+    scale, want_scale = torch.empty(tokens, device="cuda"), torch.empty(tokens, device="cuda")
+    want, want_r, want8 = torch.empty_like(near), torch.empty_like(near), torch.empty(tokens, cols, dtype=I8, device="cuda")
+    eq.eq_add_rmsnorm(near, None, 1e-5, want, residual=near, residual_out=want_r)
+    eq.eq_add_rmsnorm(x, None, 1e-5, o, residual=r, residual_out=ro)
+    eq.eq_silu_mul(near, near, want8, out_scale=want_scale)
+    eq.eq_silu_mul(x, r, o8, out_scale=scale)
+    torch.cuda.synchronize()
+    assert torch.equal(o, want) and torch.equal(ro, want_r) and torch.equal(o8, want8) and torch.equal(scale, want_scale)
+    del x, r, ro, o, o8
+    torch.cuda.empty_cache()
+
+
 def test_norm_rows_of_zeros_and_tiny_values():
     log("case norm zeros")
     for scale_of, cols in ((0.0, 100), (2.0 ** -110, 100), (2.0 ** -140, 64)):

@@ -182,6 +182,35 @@ def test_single_columns(kind, zeros, xt):
     assert torch.equal(y.cpu().double(), w.w.t())
 
 
+def test_offsets_past_32_bits():
+    """A matrix of more than 2^32 bytes of codes, x and y rows more than 2^32 bytes apart."""
+    rows, cols, group = 140000, 65536, 128
+    log("case w4 large offsets")
+    g = torch.Generator(device="cuda").manual_seed(11)
+    codes = torch.empty(rows, cols // 2, dtype=torch.uint8, device="cuda")
+    for at in range(0, rows, 20000):
+        codes[at:at + 20000].random_(0, 256, generator=g)
+    scales = (2.0 ** torch.randint(-3, 2, (rows, cols // group), generator=g, device="cuda")).to(BF16)
+    block = eq.W4Block([eq.W4Tensor(codes, scales, group=group)])
+    assert block.tensors[0].codes.numel() > 1 << 32
+    sample = torch.cat([torch.arange(40), torch.randint(0, rows, (200,), generator=gen(1)), torch.arange(rows - 40, rows)]).cuda()
+    c = codes[sample]
+    q = torch.stack([c & 15, c >> 4], dim=2).flatten(1).to(torch.int16)
+    w = torch.where(q > 7, q - 16, q).double() * scales[sample].double().repeat_interleave(group, dim=1)
+    del codes
+    for tokens in (1, 3):  # 3 rows of x and y in buffers of about 13 GB
+        step = (1 << 31) + 64
+        x = torch.empty((tokens - 1) * step + cols, dtype=BF16, device="cuda")
+        y = torch.empty((tokens - 1) * (step // 2) + rows, dtype=F32, device="cuda")
+        xv, yv = x.as_strided((tokens, cols), (step, 1)), y.as_strided((tokens, rows), (step // 2, 1))
+        xv.copy_(torch.randint(-2, 3, (tokens, cols), generator=g, device="cuda"))
+        eq.eq_w4_matvec(block, [xv], [yv])
+        torch.cuda.synchronize()
+        assert torch.equal(yv[:, sample].double(), xv.double() @ w.t())
+        del x, y, xv, yv
+    torch.cuda.empty_cache()
+
+
 def test_kinds_mixed_in_one_call():
     """Tensors of several kinds and widths, more than fit one launch."""
     log("case w4 mixed kinds")

@@ -116,6 +116,8 @@ def test_w4_matvec_refusals():
     assert matvec([t], [m(E4M3, 128, scale=P)], [y]) == eq.EQ_EUNSUPPORTED
     assert matvec([w4(dtype=E2M1)], [m(I8, 128, scale=P)], [y]) == eq.EQ_EUNSUPPORTED
     assert matvec([t], [x], [y], tokens=64 * 65535 + 1) == eq.EQ_EINVAL
+    assert matvec([w4(rows=8388593)], [x], [m(F32, 1 << 32)]) == eq.EQ_EINVAL
+    assert matvec([w4(rows=8388592)], [x], [m(F32, 1 << 32)], tokens=0) == eq.EQ_OK
     assert matvec([t], [m(BF16, 128, d=0)], [m(F32, 32, d=0)], tokens=0) == eq.EQ_OK
     assert L.eq_w4_matvec(None, 0, None, None, 2, None) == eq.EQ_OK
 
