@@ -487,7 +487,8 @@ eq_status eq_w4_pack(const eq_w4_tensor *t, const uint8_t *d_codes, const uint16
  * eq_w4_matvec -- for every tensor i: y_i[t, r] = sum_c W_i[r, c] * x_i[t, c]
  * for all tokens t, as one kernel launch for up to EQ_MAX_BLOCK_TENSORS
  * tensors of one kind (type, group, zeros, x and y types). Made for few
- * tokens: up to 64 read the weights once, more are taken 64 at a time.
+ * tokens: they are taken 64 at a time, fewer at a time where the matrices
+ * are too small to fill the GPU with one pass.
  * x: host array of n_tensors matrices [tokens, cols_i], BF16, or INT8 with
  *    INT4 weights, or E4M3 with E2M1 weights (the 8-bit forms as
  *    eq_add_rmsnorm and eq_silu_mul write them). y: host array of n_tensors

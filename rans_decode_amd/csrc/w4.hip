@@ -63,6 +63,7 @@ struct W4Args {
 struct W4Launch {
     uint32_t wg_begin[EQ_MAX_BLOCK_TENSORS];  // first workgroup of each tensor, 2^32 - 1 past the last
     uint32_t tokens;
+    uint32_t per_pass;  // tokens of a pass over the weights (grid y)
     uint32_t y_f32;
     W4Args t[EQ_MAX_BLOCK_TENSORS];
 };
@@ -226,23 +227,49 @@ struct Kind<EQ_DTYPE_INT4, EQ_DTYPE_INT8, 32, Z> {  // groups of 32: 32 columns 
     static __device__ __forceinline__ float value(int32_t d, int32_t sum_x, float zero) { return int8_value<Z>(d, sum_x, zero); }
 };
 
-// Activations at p, of which `left` elements of X exist (FULL: all of them);
-// the rest reads as zero.
-template <uint32_t X, typename Raw, bool FULL>
-__device__ __forceinline__ Raw load_raw(const char *p, int32_t left) {
-    constexpr int32_t XB = X == EQ_DTYPE_BF16 ? 2 : 1, N = sizeof(Raw) / XB;
-    if (FULL || left >= N) {
-        if constexpr (XB == 2) return *reinterpret_cast<const u32x4_a2 *>(p);
-        else if constexpr (sizeof(Raw) == 16) return *reinterpret_cast<const u32x4_a1 *>(p);
-        else return *reinterpret_cast<const u32x2_a1 *>(p);
+// Activations at p.
+template <uint32_t X, typename Raw>
+__device__ __forceinline__ Raw load_raw(const char *p) {
+    if constexpr (X == EQ_DTYPE_BF16) return *reinterpret_cast<const u32x4_a2 *>(p);
+    else if constexpr (sizeof(Raw) == 16) return *reinterpret_cast<const u32x4_a1 *>(p);
+    else return *reinterpret_cast<const u32x2_a1 *>(p);
+}
+
+// The same from column `at` of a row of `cols`; what lies past its end reads
+// as zero: the row's last values are loaded as one piece and shifted down.
+// (Loaded value by value, each piece was waited for: 36 tokens of 91 columns
+// took 13.5 us, so 12.7.)
+template <uint32_t X, typename Raw>
+__device__ __forceinline__ Raw load_raw_tail(const char *row, uint32_t at, uint32_t cols) {
+    constexpr uint32_t XB = X == EQ_DTYPE_BF16 ? 2 : 1, N = sizeof(Raw) / XB, B = sizeof(Raw);
+    if (cols < N) {  // rows shorter than a piece
+        Raw r = {};
+        for (uint32_t i = 0; i < N; ++i)
+            if (at + i < cols) {
+                const uint32_t v = XB == 2 ? reinterpret_cast<const uint16_t *>(row)[at + i]
+                                           : reinterpret_cast<const uint8_t *>(row)[at + i];
+                r[i * XB / 4] |= v << (8 * (i * XB % 4));
+            }
+        return r;
     }
-    Raw r = {};
-    for (int32_t i = 0; i < N; ++i)
-        if (i < left) {
-            const uint32_t v = XB == 2 ? reinterpret_cast<const uint16_t *>(p)[i] : reinterpret_cast<const uint8_t *>(p)[i];
-            r[i * XB / 4] |= v << (8 * (i * XB % 4));
+    const uint32_t from = at < cols - N ? at : cols - N;
+    const Raw v = load_raw<X, Raw>(row + (uint64_t)from * XB);
+    const uint32_t by = (at - from) * XB;  // bytes to shift down; B or more: nothing is left
+    uint64_t lo = (uint64_t)v[1] << 32 | v[0];
+    if constexpr (B == 8) {
+        lo = by < 8 ? lo >> (8 * by) : 0;
+        return Raw{(uint32_t)lo, (uint32_t)(lo >> 32)};
+    } else {
+        uint64_t hi = (uint64_t)v[3] << 32 | v[2];
+        if (by >= 8) {
+            lo = by < 16 ? hi >> (8 * (by - 8)) : 0;
+            hi = 0;
+        } else if (by) {
+            lo = lo >> (8 * by) | hi << (64 - 8 * by);
+            hi >>= 8 * by;
         }
-    return r;
+        return Raw{(uint32_t)lo, (uint32_t)(lo >> 32), (uint32_t)hi, (uint32_t)(hi >> 32)};
+    }
 }
 
 // What a wave reads of the weights of one column of tiles: R rows of tiles.
@@ -341,7 +368,7 @@ __global__ void __launch_bounds__(64 * kWaves) k_w4(W4Launch a) {
     const uint32_t rw = wave >> T.kw_log2, kw = wave & (kw_n - 1);
     const uint32_t row_tiles = T.row_tiles, k_tiles = T.k_tiles, k_full = T.cols / kTileCols;
     const uint32_t wg_tile = (blockIdx.x - a.wg_begin[ti]) * rw_n * R;
-    const uint32_t token0 = blockIdx.y * kMaxTokens;
+    const uint32_t token0 = blockIdx.y * a.per_pass;
 
     const char *x_row[NT];
     for (int n = 0; n < NT; ++n) {
@@ -367,16 +394,14 @@ __global__ void __launch_bounds__(64 * kWaves) k_w4(W4Launch a) {
 #pragma unroll
         for (int n = 0; n < NT; ++n)
             for (uint32_t l = 0; l < NL; ++l)
-                st.x[n][l] = load_raw<X, typename K::Raw, true>(x_row[n] + ((uint64_t)kt * kTileCols + x_col[l]) * XB, 0);
+                st.x[n][l] = load_raw<X, typename K::Raw>(x_row[n] + ((uint64_t)kt * kTileCols + x_col[l]) * XB);
     };
     auto load_tail = [&](St &st, uint32_t kt) {
         st.w.load(T, base, kt, k_tiles, lane);
 #pragma unroll
         for (int n = 0; n < NT; ++n)
-            for (uint32_t l = 0; l < NL; ++l) {
-                const uint32_t at = kt * kTileCols + x_col[l];
-                st.x[n][l] = load_raw<X, typename K::Raw, false>(x_row[n] + (uint64_t)at * XB, (int32_t)(T.cols - at));
-            }
+            for (uint32_t l = 0; l < NL; ++l)
+                st.x[n][l] = load_raw_tail<X, typename K::Raw>(x_row[n], kt * kTileCols + x_col[l], T.cols);
     };
 
     Acc acc[NT][R] = {};
@@ -513,7 +538,7 @@ __global__ void __launch_bounds__(64 * kWaves) k_w4_wide(W4Launch a) {
     const W4Args &T = a.t[ti];
     const uint32_t row_tiles = T.row_tiles, k_tiles = T.k_tiles;
     const uint32_t chunks = T.cols / (C * kTileCols);  // whole ones
-    const uint32_t token0 = blockIdx.y * kMaxTokens;
+    const uint32_t token0 = blockIdx.y * a.per_pass;
     const uint32_t want = ((blockIdx.x - a.wg_begin[ti]) * kWaves + wave) * R;  // as in k_w4
     const uint32_t tile0 = want + R <= row_tiles ? want : row_tiles - R;
     const uint64_t base = (uint64_t)tile0 * k_tiles;
@@ -537,7 +562,7 @@ __global__ void __launch_bounds__(64 * kWaves) k_w4_wide(W4Launch a) {
     typename KS::Raw raw[kLoads];
     auto load_x = [&](uint32_t chunk) {
         for (uint32_t i = 0; i < kLoads; ++i)
-            raw[i] = load_raw<X, typename KS::Raw, true>(x_at[i] + (uint64_t)chunk * (C * kTileCols * XB), 0);
+            raw[i] = load_raw<X, typename KS::Raw>(x_at[i] + (uint64_t)chunk * (C * kTileCols * XB));
     };
     auto put_x = [&](uint32_t buf) {
         typename K::Op(*to)[64] = &xs[buf][0][0][0];
@@ -630,8 +655,7 @@ __global__ void __launch_bounds__(64 * kWaves) k_w4_wide(W4Launch a) {
     }
     if (ragged < k_tiles) {
         for (uint32_t i = 0; i < kLoads; ++i)
-            raw[i] = load_raw<X, typename KS::Raw, false>(x_at[i] + (uint64_t)ragged * (kTileCols * XB),
-                                                          (int32_t)(T.cols - ragged * kTileCols) - (int32_t)x_col[i]);
+            raw[i] = load_raw_tail<X, typename KS::Raw>(x_at[i] - (uint64_t)x_col[i] * XB, ragged * kTileCols + x_col[i], T.cols);
         put_x(0);
         __syncthreads();
 #pragma unroll
@@ -752,6 +776,13 @@ bool tensor_ok(const eq_w4_tensor &t) {
     return aligned(t.d_codes, 16) && aligned(t.d_scales, 8) && aligned(t.d_zeros, 4);
 }
 
+// Waves that share out the columns (log2): as many as have two tiles each.
+uint32_t kw_log2(uint32_t k_tiles) {
+    uint32_t n = 3;
+    while (n > 0 && k_tiles < (2u << n)) --n;
+    return n;
+}
+
 struct Shape {
     uint32_t nt, tp, r;  // token tiles of tp (4, 8 or 16) tokens and rows of tiles per wave
     bool wide;           // k_w4_wide
@@ -770,21 +801,20 @@ struct Shape {
 //    28.3, k_w4 25.8), 32 from 1536 (3584: int8 48.0, k_w4 58.6; 1280: 37.4,
 //    36.9), 64 from 1024 (3584: int8 57.5, k_w4 112; 688: bf16 33.0, 29.7);
 //    there r = 2 from 2560 (3584, 64 tokens int8: 62, one 69; 1792: 51, 41).
-Shape shape(uint64_t tokens, uint64_t row_tiles, uint64_t fewest) {
-    const uint32_t nt = tokens <= 16 ? 1 : tokens <= 32 ? 2 : 4;
+//  * with fewer than 512 workgroups of one row of tiles a wave, the tokens are
+//    spread over passes of 32 or 16 (64 tokens int8 x 1024 x 8192: 6.4, one pass
+//    14.4; bf16 x 4096 x 4096: 10.1, 15.4; 1024 instead of 512: 8192 x 28672 int8
+//    63.8 against 48.9).
+Shape shape(uint64_t tokens, uint64_t row_tiles, uint64_t fewest, uint32_t kw_log2) {
+    uint32_t nt = tokens <= 16 ? 1 : tokens <= 32 ? 2 : 4;
     const uint32_t tp = tokens <= 4 ? 4 : tokens <= 8 ? 8 : 16;
     if (tokens > 8 && fewest >= 2 && row_tiles >= (nt == 1 ? 2560 : nt == 2 ? 1536 : 1024))
         return {nt, tp, row_tiles >= 2560 ? 2u : 1u, true};
-    uint32_t r = tokens == 1 ? 1 : tokens <= 8 || nt == 4 || row_tiles < 640 ? 2 : 4;
-    while (r > 1 && (row_tiles < 128 * r || fewest < r)) r /= 2;
+    const uint64_t wgs = ((row_tiles << kw_log2) + kWaves - 1) / kWaves;  // with one row of tiles a wave
+    while (nt > 1 && wgs * ((tokens + 16 * nt - 1) / (16 * nt)) < 512) nt /= 2;
+    uint32_t r = tokens == 1 ? 1 : tokens <= 8 || nt == 4 || wgs < 640 ? 2 : 4;
+    while (r > 1 && (wgs < 128 * r || fewest < r)) r /= 2;
     return {nt, tp, r, false};
-}
-
-// Waves that share out the columns (log2): as many as have two tiles each.
-uint32_t kw_log2(uint32_t k_tiles) {
-    uint32_t n = 3;
-    while (n > 0 && k_tiles < (2u << n)) --n;
-    return n;
 }
 
 W4Args tensor_args(const eq_w4_tensor &t) {
@@ -855,14 +885,17 @@ eq_status eq_w4_matvec(const eq_w4_tensor *tensors, uint32_t n_tensors, const eq
         if (before % EQ_MAX_BLOCK_TENSORS) continue;
         uint32_t which[EQ_MAX_BLOCK_TENSORS], n = 0;
         uint64_t total = 0, fewest = ~0ull;  // rows of tiles
+        uint32_t kw = 0;
         for (uint32_t i = first; i < n_tensors && n < EQ_MAX_BLOCK_TENSORS; ++i) {
             if (kind(i) != kind(first)) continue;
             which[n++] = i;
             const uint64_t rt = (tensors[i].rows + kTileRows - 1) / kTileRows;
             total += rt;
             fewest = rt < fewest ? rt : fewest;
+            const uint32_t k = kw_log2((uint32_t)((tensors[i].cols + kTileCols - 1) / kTileCols));
+            kw = k > kw ? k : kw;
         }
-        const Shape sh = shape(tokens, total, fewest);
+        const Shape sh = shape(tokens, total, fewest, kw);
         W4Launch a{};
         uint64_t wgs = 0;
         for (uint32_t k = 0; k < EQ_MAX_BLOCK_TENSORS; ++k) a.wg_begin[k] = ~0u;
@@ -880,7 +913,8 @@ eq_status eq_w4_matvec(const eq_w4_tensor *tensors, uint32_t n_tensors, const eq
             const uint64_t per_wg = (kWaves >> t.kw_log2) * sh.r;
             wgs += (t.row_tiles + per_wg - 1) / per_wg;
         }
-        const uint64_t passes = (tokens + kMaxTokens - 1) / kMaxTokens;
+        a.per_pass = sh.tp < 16 ? kMaxTokens : 16 * sh.nt;
+        const uint64_t passes = (tokens + a.per_pass - 1) / a.per_pass;
         a.tokens = (uint32_t)tokens;
         a.y_f32 = y[first].dtype == EQ_DTYPE_F32;
         hipLaunchKernelGGL(pick(tensors[first].dtype, x[first].dtype, tensors[first].d_zeros != nullptr,

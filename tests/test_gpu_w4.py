@@ -211,6 +211,12 @@ def test_offsets_past_32_bits():
     torch.cuda.empty_cache()
 
 
+def test_very_many_tokens_exact():
+    """Passes along a grid's second dimension, near its limit, for a matrix of one workgroup."""
+    for tokens, rows, cols in ((1100000, 16, 8), (4 * 65535 + 3, 5, 130)):
+        run(31, tokens, [rows], cols, "int4", False, BF16, 32)
+
+
 def test_kinds_mixed_in_one_call():
     """Tensors of several kinds and widths, more than fit one launch."""
     log("case w4 mixed kinds")
