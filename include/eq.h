@@ -389,7 +389,9 @@ eq_status eq_bf16_from_f32(const float *d_in, uint64_t n, uint16_t *d_out, void 
 /*
  * The steps around a block's weight products (eq_add_rmsnorm, eq_silu_mul,
  * eq_w4_matvec). They only enqueue kernels: no allocation, no workspace, no
- * synchronisation; with zero tokens nothing is enqueued. Results do not
+ * synchronisation; with zero tokens nothing is enqueued. Device memory and
+ * stream are the current device's (a NULL stream means its default stream;
+ * the Python binding makes the tensors' device current). Results do not
  * depend on timing (no atomics; every sum has a fixed order).
  *
  * eq_matrix: [tokens, width] activations in device memory; row t starts

@@ -331,7 +331,8 @@ def eq_bf16_from_f32(x, out, stream=None) -> None:
 
 
 # ---------------------------------------------------------------------------
-# The steps around the weight products (torch tensors on the GPU)
+# The steps around the weight products (torch tensors, all of a call on one
+# GPU, which need not be the current one)
 # ---------------------------------------------------------------------------
 _types: dict = {}  # torch's types by the library's numbers, filled at the first use of one
 
@@ -354,13 +355,29 @@ def _raw_stream():
         lambda index: torch.cuda.current_stream(index).cuda_stream)
 
 
-def _stream_of(stream, t) -> int | None:
-    return _raw_stream()(t.get_device()) if stream is None else _stream_handle(stream)
+def _enqueue(name: str, gpu: int, stream, *args) -> None:
+    """The library's call `name` on GPU `gpu` and one of its streams (None: its
+    current one). The GPU is made the current one for the call: kernels are
+    launched there, and the default stream's handle, 0 on every GPU, means its
+    default stream."""
+    if stream is None:
+        handle = _raw_stream()(gpu)
+    else:
+        on = getattr(getattr(stream, "device", None), "index", None)  # a plain handle does not say
+        if on is not None and on != gpu:
+            raise ValueError(f"{name}: a stream of cuda:{on}, tensors on cuda:{gpu}")
+        handle = _stream_handle(stream)
+    cuda = _torch().cuda
+    if cuda.current_device() == gpu:
+        _check(name, getattr(_lib, name)(*args, handle))
+    else:
+        with cuda.device(gpu):
+            _check(name, getattr(_lib, name)(*args, handle))
 
 
-def _matrix(name: str, t, tokens: int, cols: int, scale=None) -> bytes:
-    """eq_matrix of a [tokens, cols] tensor (or [cols] for one token) whose last
-    dimension is dense."""
+def _matrix(name: str, t, gpu: int, tokens: int, cols: int, scale=None) -> bytes:
+    """eq_matrix of a [tokens, cols] tensor (or [cols] for one token) on GPU
+    `gpu` whose last dimension is dense."""
     dtype = _types.get(t.dtype) or _activation_type(t.dtype)
     stride = t.stride()
     if t.shape != (tokens, cols) and (tokens != 1 or t.shape != (cols,)):
@@ -369,6 +386,8 @@ def _matrix(name: str, t, tokens: int, cols: int, scale=None) -> bytes:
         raise ValueError(f"{name}: elements of a row must be contiguous")
     if not t.is_cuda:
         raise ValueError(f"{name}: must be on the GPU")
+    if t.get_device() != gpu:
+        raise ValueError(f"{name}: on cuda:{t.get_device()}, other tensors of the call on cuda:{gpu}")
     ld = stride[0] if tokens > 1 else cols  # one row has any stride
     if dtype == EQ_DTYPE_F32 or dtype == EQ_DTYPE_BF16:
         if scale is not None:
@@ -378,8 +397,8 @@ def _matrix(name: str, t, tokens: int, cols: int, scale=None) -> bytes:
         raise ValueError(f"{name}: type {t.dtype} is not supported")
     if scale is None:
         raise ValueError(f"{name}: an 8-bit matrix needs its scales (fp32, one per row)")
-    if scale.dtype != _torch().float32 or scale.numel() != tokens or not scale.is_contiguous() or not scale.is_cuda:
-        raise ValueError(f"{name}: scales must be {tokens} contiguous fp32 values on the GPU")
+    if scale.dtype != _torch().float32 or scale.numel() != tokens or not scale.is_contiguous() or scale.get_device() != gpu:
+        raise ValueError(f"{name}: scales must be {tokens} contiguous fp32 values on the same GPU")
     return _pack_matrix(t.data_ptr(), ld, scale.data_ptr(), dtype, 0)
 
 
@@ -394,21 +413,22 @@ def eq_add_rmsnorm(x, weight, eps: float, out, out_scale=None, residual=None, re
     (default: into residual itself). out: bfloat16, or int8 / float8_e4m3fn
     with out_scale (fp32, one per token). weight: bf16 or fp32 [cols], or None."""
     tokens, cols = _size(x)
+    gpu = x.get_device()
     r = ro = w = None
     w_type = 0
     if residual is not None:
-        r = _matrix("residual", residual, tokens, cols)
-        ro = r if residual_out is None else _matrix("residual_out", residual_out, tokens, cols)
+        r = _matrix("residual", residual, gpu, tokens, cols)
+        ro = r if residual_out is None else _matrix("residual_out", residual_out, gpu, tokens, cols)
     elif residual_out is not None:
         raise ValueError("residual_out without a residual")
     if weight is not None:
         w_type = _activation_type(weight.dtype)
-        if weight.numel() != cols or not weight.is_contiguous() or not weight.is_cuda:
-            raise ValueError(f"weight: {cols} contiguous values on the GPU")
+        if weight.numel() != cols or not weight.is_contiguous() or not weight.is_cuda \
+                or weight.get_device() != gpu:
+            raise ValueError(f"weight: {cols} contiguous values on x's GPU")
         w = weight.data_ptr()
-    _check("eq_add_rmsnorm", _lib.eq_add_rmsnorm(
-        _matrix("x", x, tokens, cols), r, ro, w, w_type, eps, tokens, cols,
-        _matrix("out", out, tokens, cols, out_scale), _stream_of(stream, x)))
+    _enqueue("eq_add_rmsnorm", gpu, stream, _matrix("x", x, gpu, tokens, cols), r, ro, w, w_type, eps, tokens, cols,
+             _matrix("out", out, gpu, tokens, cols, out_scale))
 
 
 def eq_silu_mul(gate, up, out, out_scale=None, stream=None) -> None:
@@ -416,17 +436,17 @@ def eq_silu_mul(gate, up, out, out_scale=None, stream=None) -> None:
     bf16, rows may be strided: two halves of one buffer). out and out_scale as
     for eq_add_rmsnorm."""
     tokens, cols = _size(gate)
-    _check("eq_silu_mul", _lib.eq_silu_mul(
-        _matrix("gate", gate, tokens, cols), _matrix("up", up, tokens, cols), tokens, cols,
-        _matrix("out", out, tokens, cols, out_scale), _stream_of(stream, gate)))
+    gpu = gate.get_device()
+    _enqueue("eq_silu_mul", gpu, stream, _matrix("gate", gate, gpu, tokens, cols), _matrix("up", up, gpu, tokens, cols),
+             tokens, cols, _matrix("out", out, gpu, tokens, cols, out_scale))
 
 
 class W4Tensor:
     """A 4-bit weight matrix in the kernels' layout (eq_w4_pack), on the device
     of `codes`: uint8 [rows, ceil(cols / 2)], column 2i in the lower half of
     byte i; scales bfloat16 and zeros uint8 (INT4, optional)
-    [rows, ceil(cols / group)]. The arrays are written on the current stream;
-    order other streams after it."""
+    [rows, ceil(cols / group)]. The arrays are written on that
+    device's current stream; order other streams after it."""
 
     def __init__(self, codes, scales, zeros=None, dtype: int = EQ_DTYPE_INT4, group: int = 128,
                  cols: int | None = None):
@@ -455,9 +475,9 @@ class W4Tensor:
         self.c = eq_w4_tensor(dtype=dtype, group=group, rows=rows, cols=cols, d_codes=self.codes.data_ptr(),
                               d_scales=self.scales.data_ptr(),
                               d_zeros=self.zeros.data_ptr() if zeros is not None else None)
-        _check("eq_w4_pack", _lib.eq_w4_pack(
-            ctypes.byref(self.c), codes.data_ptr(), scales.data_ptr(),
-            zeros.data_ptr() if zeros is not None else None, _stream_of(None, codes)))
+        self.gpu = codes.get_device()
+        _enqueue("eq_w4_pack", self.gpu, None, ctypes.byref(self.c), codes.data_ptr(), scales.data_ptr(),
+                 zeros.data_ptr() if zeros is not None else None)
 
     @property
     def nbytes(self) -> int:
@@ -483,11 +503,14 @@ def eq_w4_matvec(block: W4Block, xs, ys, x_scales=None, stream=None) -> None:
         raise ValueError("one x, one y and, with scales, one x_scales entry per tensor")
     if n == 0:
         return
-    tokens = _size(xs[0])[0]
-    xm = b"".join([_matrix("x", x, tokens, t.cols, x_scales[i] if x_scales is not None else None)
+    tokens, gpu = _size(xs[0])[0], xs[0].get_device()
+    for t in tensors:
+        if t.gpu != gpu:
+            raise ValueError(f"x on {xs[0].device}, weights on cuda:{t.gpu}")
+    xm = b"".join([_matrix("x", x, gpu, tokens, t.cols, x_scales[i] if x_scales is not None else None)
                    for i, (t, x) in enumerate(zip(tensors, xs))])
-    ym = b"".join([_matrix("y", y, tokens, t.rows) for t, y in zip(tensors, ys)])
-    _check("eq_w4_matvec", _lib.eq_w4_matvec(block.c, n, xm, ym, tokens, _stream_of(stream, xs[0])))
+    ym = b"".join([_matrix("y", y, gpu, tokens, t.rows) for t, y in zip(tensors, ys)])
+    _enqueue("eq_w4_matvec", gpu, stream, block.c, n, xm, ym, tokens)
 
 
 class Pipeline:
