@@ -496,9 +496,16 @@ eq_status eq_w4_pack(const eq_w4_tensor *t, const uint8_t *d_codes, const uint16
  *    eq_add_rmsnorm and eq_silu_mul write them). y: host array of n_tensors
  *    matrices [tokens, rows_i], F32 or BF16, overlapping nothing else.
  * Arithmetic: exact products, fp32 accumulation (int32 within a group for
- *    INT8 x); one rounding at the end for BF16 y. A token's y depends on no
- *    other token's x; deterministic, but not bit-reproducible against other
- *    summation orders or token counts.
+ *    INT8 x), the 8-bit forms' x scale at the end; one rounding at the end for
+ *    BF16 y. |y - W x| <= (cols + 16) 2^-24 sum |scale| |x| b, b = |q| for E2M1
+ *    and, for INT4 with INT8 x, |q| + |zero|. INT4 with BF16 x is summed as
+ *    16 + u with u the unsigned code (signed q: q + 8, and zero 8), less
+ *    (16 + zero) sum x: b = (16 + u) + (16 + zero), and where W x is 0 y is as
+ *    far from it as that. With BF16 x, y is finite wherever fp32 sums of W x
+ *    are, and an infinity in x gives the infinity or NaN that it gives in W x;
+ *    such sums are taken again, which takes several times as long. A token's
+ *    y depends on no other token's x; deterministic, but not bit-reproducible
+ *    against other summation orders or token counts.
  * Errors: EQ_EINVAL (as eq_w4_pack; a stride below the width, a missing
  *    scale array, an unknown type, more than 64 * 65535 tokens or 8388592
  *    rows), EQ_EUNSUPPORTED (INT8 x with E2M1

@@ -312,9 +312,75 @@ struct Weights {
     }
 };
 
+__device__ __forceinline__ bool not_finite(float v) { return !(fabsf(v) < __builtin_inff()); }
+
 __device__ __forceinline__ void store_y(const W4Args &T, bool f32, uint32_t t, uint32_t row, float v) {
     if (f32) static_cast<float *>(T.y)[t * T.ldy + row] = v;
     else static_cast<uint16_t *>(T.y)[t * T.ldy + row] = (uint16_t)pack_bf16(v, 0.0f);
+}
+
+// bf16 activations reach to 2^128, so the sums of a group, taken before its
+// scale and with a code's bias, can overflow (from |x| of 2^116 on, with zeros
+// from 2^112; E2M1 2^118) or meet an infinity in x that the bias turns into
+// inf - inf, although W x is a number or one infinity. A wave whose outputs are
+// not all finite therefore looks at them again (y[t, its rows of one tile])
+// and sums those with W = (q - zero) * scale itself, which fp32 holds exactly:
+// lane (row, quarter) takes the words that it loads in the products, and the
+// four quarters join in order. A NaN in x's row leaves nothing to look for.
+// The check, one comparison per output, costs up to 2% (64 tokens x 11008 x
+// 4096, group 32: 33.3 us, 32.6 without; one token within noise). One token
+// through 57344 x 8192: 36 us, with an infinity in x 231, with a NaN 50.
+template <uint32_t W, uint32_t S, bool Z>
+__device__ __forceinline__ void sum_again(const W4Args &T, bool f32, uint32_t t, uint32_t row_tile) {
+    constexpr uint32_t P = kTileCols / S;
+    // counted anew, and another value to the compiler than the products' lane:
+    // what the two shared was kept in registers all through the products
+    uint32_t lane = __builtin_amdgcn_mbcnt_hi(~0u, __builtin_amdgcn_mbcnt_lo(~0u, 0));
+    asm volatile("" : "+v"(lane));
+    const uint32_t i16 = lane & 15u, quarter = lane >> 4, row = row_tile * kTileRows + i16;
+    bool bad = false;
+    if (row < T.rows) {
+        const uint64_t at = t * T.ldy + row;
+        bad = not_finite(f32 ? static_cast<const float *>(T.y)[at] : bf16_lo(static_cast<const uint16_t *>(T.y)[at]));
+    }
+    if (!__any(bad)) return;
+    const char *x = static_cast<const char *>(T.x) + (uint64_t)t * T.ldx * 2;
+    bool nan = false;
+    for (uint64_t c = lane; c < T.cols; c += 64) nan |= (reinterpret_cast<const uint16_t *>(x)[c] & 0x7FFFu) > 0x7F80u;
+    if (__any(nan)) return;
+    float sum = 0.0f;
+#pragma unroll 1
+    for (uint32_t kt = 0; kt < T.k_tiles; ++kt) {
+        const uint64_t tile = (uint64_t)row_tile * T.k_tiles + kt;
+        float tile_sum = 0.0f;
+#pragma unroll
+        for (uint32_t j = 0; j < 4; ++j) {  // (unrolled it took more registers than the products)
+            const uint32_t word = reinterpret_cast<const uint32_t *>(T.codes + tile * 64 + lane)[j];
+            const uint32_t col = word_col(S, quarter, j);
+            const uint64_t g = (tile * kTileRows + i16) * P + col / S;
+            const float scale = bf16_lo(T.scales[g]);
+            const int32_t zero = Z ? T.zeros[g] : 0;
+            const u32x4 v = load_raw_tail<EQ_DTYPE_BF16, u32x4>(x, kt * kTileCols + col, T.cols);
+            const u32x4 floats = decode8<W, Z>(word);  // E2M1's values
+#pragma unroll
+            for (uint32_t k = 0; k < 8; ++k) {
+                float q;
+                if constexpr (W == EQ_DTYPE_INT4) {
+                    const uint32_t up = word << (28 - 4 * (k % 2 * 4 + k / 2));  // the code in the upper 4 bits
+                    q = (float)(Z ? (int32_t)(up >> 28) - zero : (int32_t)up >> 28);
+                } else {
+                    q = k % 2 ? bf16_hi(floats[k / 2]) : bf16_lo(floats[k / 2]);
+                }
+                const float xv = k % 2 ? bf16_hi(v[k / 2]) : bf16_lo(v[k / 2]);
+                // columns past the end have x = 0 and, in whole groups, scale 0
+                tile_sum = fmaf(q * scale, xv, tile_sum);
+            }
+        }
+        sum += tile_sum;
+    }
+    float total = 0.0f;
+    for (uint32_t k = 0; k < 4; ++k) total += __shfl(sum, (int)(k * 16 + i16));
+    if (bad && quarter == 0) store_y(T, f32, t, row, total);
 }
 
 // A wave's LDS accesses are performed in program order; this keeps the compiler
@@ -477,27 +543,46 @@ __global__ void __launch_bounds__(64 * kWaves) k_w4(W4Launch a) {
         compute(st);
     }
 
+    // the row of tiles of the workgroup's o-th output, none where it is another's
+    constexpr uint32_t kNone = ~0u;
+    auto row_tile_of = [&](uint32_t o) -> uint32_t {
+        const uint32_t r = o % R, t0 = wg_tile + o / R * R;
+        if (t0 + R <= row_tiles) return t0 + r;
+        return t0 >= row_tiles || row_tiles - R + r < t0 ? kNone : row_tiles - R + r;
+    };
+    bool bad = false;
 #pragma unroll
     for (int n = 0; n < NT; ++n) {
         if (n) __syncthreads();
         for (int r = 0; r < R; ++r) part[wave][r][lane] = acc[n][r];
         __syncthreads();
         for (uint32_t o = wave; o < rw_n * R; o += kWaves) {
-            const uint32_t orw = o / R, r = o % R;
-            uint32_t t0 = wg_tile + orw * R;
-            const bool moved = t0 + R > row_tiles;
-            if (moved && (t0 >= row_tiles || row_tiles - R + r < t0)) continue;  // another wave's row of tiles
-            if (moved) t0 = row_tiles - R;
+            const uint32_t row_tile = row_tile_of(o);
+            if (row_tile == kNone) continue;
             Acc s = {};
-            for (uint32_t w = 0; w < kw_n; ++w) s += part[orw * kw_n + w][r][lane];
-            const uint32_t row = (t0 + r) * kTileRows + i16;
+            for (uint32_t w = 0; w < kw_n; ++w) s += part[o / R * kw_n + w][o % R][lane];
+            const uint32_t row = row_tile * kTileRows + i16;
             for (uint32_t i = 0; i < NI; ++i) {
                 const uint32_t t = token0 + n * 16 + quarter * NI + i;
                 if (t < a.tokens && row < T.rows) {
                     float v = s[i];
                     if constexpr (X != EQ_DTYPE_BF16) v *= T.x_scale[t];
                     store_y(T, a.y_f32, t, row, v);
+                    bad |= not_finite(v);
                 }
+            }
+        }
+    }
+    if constexpr (X == EQ_DTYPE_BF16) {
+        if (__any(bad)) {
+            __threadfence_block();  // lanes read what others of the wave stored
+            const uint32_t end = token0 + TP * NT < a.tokens ? token0 + TP * NT : a.tokens;
+#pragma unroll 1
+            for (uint32_t o = wave; o < rw_n * R; o += kWaves) {
+                const uint32_t row_tile = row_tile_of(o);
+                if (row_tile == kNone) continue;
+#pragma unroll 1
+                for (uint32_t t = token0; t < end; ++t) sum_again<W, S, Z>(T, a.y_f32, t, row_tile);
             }
         }
     }
@@ -662,6 +747,7 @@ __global__ void __launch_bounds__(64 * kWaves) k_w4_wide(W4Launch a) {
         for (uint32_t d = 0; d < C; ++d)
             if (ragged + d < k_tiles) compute(w[d], 0, d);
     }
+    bool bad = false;
 #pragma unroll
     for (int r = 0; r < R; ++r) {
         const uint32_t row = (tile0 + r) * kTileRows + i16;
@@ -670,8 +756,24 @@ __global__ void __launch_bounds__(64 * kWaves) k_w4_wide(W4Launch a) {
         for (int n = 0; n < NT; ++n)
             for (int i = 0; i < 4; ++i) {
                 const uint32_t t = token0 + n * 16 + quarter * 4 + i;
-                if (t < a.tokens) store_y(T, a.y_f32, t, row, X == EQ_DTYPE_BF16 ? acc[n][r][i] : acc[n][r][i] * T.x_scale[t]);
+                if (t < a.tokens) {
+                    const float v = X == EQ_DTYPE_BF16 ? acc[n][r][i] : acc[n][r][i] * T.x_scale[t];
+                    store_y(T, a.y_f32, t, row, v);
+                    bad |= not_finite(v);
+                }
             }
+    }
+    if constexpr (X == EQ_DTYPE_BF16) {
+        if (__any(bad)) {
+            __threadfence_block();  // lanes read what others of the wave stored
+            const uint32_t end = token0 + 16 * NT < a.tokens ? token0 + 16 * NT : a.tokens;
+#pragma unroll 1
+            for (uint32_t r = 0; r < R; ++r) {
+                if (tile0 + r < want) continue;
+#pragma unroll 1
+                for (uint32_t t = token0; t < end; ++t) sum_again<W, S, Z>(T, a.y_f32, t, tile0 + r);
+            }
+        }
     }
 }
 
