@@ -404,7 +404,7 @@ eq_status eq_bf16_from_f32(const float *d_in, uint64_t n, uint16_t *d_out, void 
  * from the fp32 result v of the row: a = max(max_c |v[t, c]|, 2^-96),
  * d_scale[t] = a / L and code = round(v * (L / a)) with L = 127 (int8) or 448
  * (E4M3FN), to nearest, ties to even. A row that holds an infinity or a NaN
- * gets a scale that is one (its values are then not meaningful).
+ * gets a scale that is an infinity or a NaN (its codes then mean nothing).
  */
 typedef struct eq_matrix {
     void *d;           /* device pointer to element [0, 0]; not written where it is an input */
@@ -425,7 +425,10 @@ typedef struct eq_matrix {
  *    NULL for ones. out: BF16, INT8 or E4M3 (see eq_matrix); it must not
  *    overlap any other argument.
  * Arithmetic: s^2 summed in fp32; out = (s * weight) * (1 / sqrt(...)) in
- *    fp32, rounded once.
+ *    fp32, rounded once. Rows whose squares, their mean or s * weight leave
+ *    fp32's range (|s| beyond about 2^63, or below 2^-45 throughout with an eps
+ *    that does not cover it) are computed again times a power of two. A row of
+ *    zeros with eps 0 gives NaN, as 0 / 0 is.
  * Errors: EQ_EINVAL (NULL, a type not listed, cols 0 or above 2^31 - 1,
  *    tokens above 2^31 - 1, a stride below cols, only one of residual and
  *    residual_out, a missing scale array, eps negative or NaN), EQ_EHIP.

@@ -6,7 +6,9 @@
 //   norm: s = x + r; y = (s * w) * R, R = 1 / sqrt(mean(s^2) + eps).
 //     R > 0 scales the whole row, so max|y| = max|s * w| * R (rounding is
 //     monotone): the sum of squares and the 8-bit scale's maximum come out of
-//     ONE reduction, and a row is read once.
+//     ONE reduction, and a row is read once. Where mean(s^2) + eps or s * w
+//     leaves fp32's range the row is read again (see in_range); its output is
+//     of ordinary size all the same.
 //   silu: y = g * (1 / (1 + exp(-g))) * u, with the hardware's exp2 and
 //     reciprocal (1 ulp each; the exponent's product with log2 e adds at most
 //     |g| 2^-24 relative, and 1 / (1 + exp(-g)) is insensitive to it for
@@ -132,7 +134,7 @@ __device__ __forceinline__ void join(float &sum, uint32_t &top) {
 }
 
 // Sum and maximum over the workgroup, in a fixed order; every thread gets
-// both. `lds` holds one pair per wave.
+// both (what is not used is not computed). `lds` holds one pair per wave.
 __device__ __forceinline__ void reduce(float &sum, uint32_t &top, float *lds_sum, uint32_t *lds_top) {
     join<0xB1>(sum, top);   // quad_perm 1 0 3 2
     join<0x4E>(sum, top);   // quad_perm 2 3 0 1
@@ -167,6 +169,17 @@ enum Op : uint32_t { NORM, SILU };
 
 __device__ __forceinline__ float silu(float g) { return g * __builtin_amdgcn_rcpf(1.0f + __expf(-g)); }
 
+// Whether a norm's sums can be used: squares overflow from |s| of 2^64 on, below
+// 2^-63 they lose bits (which matters where eps does not cover them), and s * w
+// may overflow although s * R * w does not. A row out of range is summed again
+// times 2^-80 or 2^80, a factor that R takes back: with 2^-80 up to 2^31 squares
+// of the largest s stay below 2^128. (Infinities and NaN come out the same.)
+// bf16 outputs need no maximum over the row: a thread that stored an infinity
+// takes (s * R) * w instead. (Looked for ahead of the reduction it cost 18
+// registers and 1777 rows of 5003 29%.)
+constexpr float kMeanLow = 0x1p-90f, kMeanHigh = 0x1p126f, kRescale = 0x1p80f;
+constexpr uint32_t kInf = 0x7F800000u;
+
 __device__ __forceinline__ void join_top(uint32_t &top, float v) {
     const uint32_t b = __float_as_uint(v) & 0x7FFFFFFFu;
     top = top > b ? top : b;
@@ -174,8 +187,10 @@ __device__ __forceinline__ void join_top(uint32_t &top, float v) {
 
 // The row's values before its common factor: s * w (norm, squares of s added
 // to sum) or the finished y (silu); top joins the patterns of their |value|.
-// RES: 0 none, else EQ_DTYPE_BF16 / EQ_DTYPE_F32.
-template <uint32_t OP, bool XF32, uint32_t RES>
+// RES: 0 none, else EQ_DTYPE_BF16 / EQ_DTYPE_F32. A second reading of a norm's
+// row: SCALED takes s times k, FINAL (s * k * f) * w.
+enum Scales : uint32_t { UNSCALED, SCALED, FINAL };
+template <uint32_t OP, bool XF32, uint32_t RES, uint32_t SCALES = UNSCALED>
 struct Row {
     static constexpr bool RF32 = OP == SILU ? XF32 : RES == EQ_DTYPE_F32;
     static constexpr size_t XB = XF32 ? 4 : 2, RB = RF32 ? 4 : 2;
@@ -183,10 +198,15 @@ struct Row {
     char *r_out;
     const void *w;
     bool w_f32;
+    float k, f;
 
-    __device__ __forceinline__ Row(const RowArgs &a, uint64_t row)
+    __device__ __forceinline__ Row(const RowArgs &a, uint64_t row, float scale = 1.0f, float factor = 1.0f)
         : x(static_cast<const char *>(a.x) + row * a.ldx * XB), r(static_cast<const char *>(a.r) + row * a.ldr * RB),
-          r_out(static_cast<char *>(a.r_out) + row * a.ldro * RB), w(a.w), w_f32(a.w_f32) {}
+          r_out(static_cast<char *>(a.r_out) + row * a.ldro * RB), w(a.w), w_f32(a.w_f32), k(scale), f(factor) {}
+
+    __device__ __forceinline__ float scaled(float s) const {
+        return SCALES == FINAL ? s * k * f : SCALES == SCALED ? s * k : s;
+    }
 
     __device__ __forceinline__ void values8(uint32_t at, float (&v)[kChunk], float &sum, uint32_t &top) const {
         load8<XF32>(x, at, v);
@@ -207,6 +227,7 @@ struct Row {
                     for (uint32_t i = 0; i < kChunk; ++i) v[i] = from_bits<false>(bf16_bits(v[i]));
                 }
             }
+            for (uint32_t i = 0; i < kChunk; ++i) v[i] = scaled(v[i]);
             for (uint32_t i = 0; i < kChunk; ++i) sum = fmaf(v[i], v[i], sum);
             if (w) {
                 float t[kChunk];
@@ -242,6 +263,7 @@ struct Row {
                     v = from_bits<false>(h);
                 }
             }
+            v = scaled(v);
             sum = fmaf(v, v, sum);
             if (w) v *= __uint_as_float(b.w);
         }
@@ -255,8 +277,12 @@ struct Row {
 // there is one, else from x). The last cols % 8 values go to one thread each,
 // their loads ahead of the chunks' (a chunk of its own for them, filled value
 // by value, cost rows of 5003 bf16 20%).
+// At least 7 waves a SIMD are asked for where a norm to bf16 without a residual
+// holds three chunks: by itself the compiler takes 73 registers, one more than 7
+// waves have, and with the request 48 (1777 rows of 5003: 15.1 us, 11.3 with it).
 template <uint32_t OP, bool XF32, uint32_t RES, uint32_t OUT, int NV>
-__global__ void __launch_bounds__(kMaxThreads) k_row(RowArgs a) {
+__global__ void __launch_bounds__(kMaxThreads, OP == NORM && RES == 0 && OUT == EQ_DTYPE_BF16 && NV == 3 ? 7 : 4)
+k_row(RowArgs a) {
     typedef Row<OP, XF32, RES> In;
     __shared__ float lds_sum[kMaxThreads / 64];
     __shared__ uint32_t lds_top[kMaxThreads / 64];
@@ -280,10 +306,50 @@ __global__ void __launch_bounds__(kMaxThreads) k_row(RowArgs a) {
         for (uint64_t at = first; at < whole; at += step) in.values8((uint32_t)at, v[0], sum, top);
     }
     if (extra) v1 = in.value1(last, bits, sum, top);
-    float factor = 1.0f, inv = 1.0f;
+
+    // A second reading (take(at, 8 values) and take1(at, value) for all of this
+    // thread's): a norm's reads the stored sum, where there is one, which is what
+    // this thread itself stored.
+    auto read_again = [&](auto scales, float k, float f, float &sum2, uint32_t &top2, auto take, auto take1) {
+        typedef Row<OP, RES ? RES == EQ_DTYPE_F32 : XF32, 0, OP == NORM ? (uint32_t)scales() : UNSCALED> Again;
+        RowArgs b = a;
+        if constexpr (RES != 0) {
+            b.x = a.r_out;
+            b.ldx = a.ldro;
+        }
+        const Again again(b, row, k, f);
+        uint32_t from = first;
+        // or the first reading's addresses are kept for it, at the cost of a workgroup a unit
+        asm volatile("" : "+v"(from));
+        const uint32_t from1 = whole + from / kChunk;
+#pragma unroll 1
+        for (uint64_t at = from; at < whole; at += step) {
+            float t[kChunk];
+            again.values8((uint32_t)at, t, sum2, top2);
+            take((uint32_t)at, t);
+        }
+        if (from1 < a.cols) take1(from1, again.value1(from1, again.load1(from1), sum2, top2));
+    };
+
+    float factor = 1.0f, inv = 1.0f, k = 1.0f;
+    bool twice = NV == 0;  // whether the output takes a second reading
     if constexpr (OP == NORM || OUT != EQ_DTYPE_BF16) {
         reduce(sum, top, lds_sum, lds_top);
-        if constexpr (OP == NORM) factor = rsqrtf(sum / (float)a.cols + a.eps);
+        if constexpr (OP == NORM) {
+            float mean = sum / (float)a.cols + a.eps;
+            const bool in_range = mean >= kMeanLow && mean <= kMeanHigh && (OUT == EQ_DTYPE_BF16 || top < kInf);
+            if (!__builtin_amdgcn_readfirstlane(in_range)) {  // the same in all threads
+                k = mean < kMeanLow ? kRescale : 1.0f / kRescale;
+                sum = 0.0f;
+                top = 0;
+                read_again([] { return SCALED; }, k, 1.0f, sum, top, [](uint32_t, float(&)[kChunk]) {}, [](uint32_t, float) {});
+                __syncthreads();  // the first sums have been read
+                reduce(sum, top, lds_sum, lds_top);
+                mean = sum / (float)a.cols + a.eps * k * k;
+                twice = true;
+            }
+            factor = rsqrtf(mean);
+        }
         if constexpr (OUT != EQ_DTYPE_BF16) {
             constexpr float L = OUT == EQ_DTYPE_INT8 ? 127.0f : 448.0f;
             float amax = __uint_as_float(top) * factor;
@@ -294,30 +360,40 @@ __global__ void __launch_bounds__(kMaxThreads) k_row(RowArgs a) {
     }
     constexpr size_t OB = OUT == EQ_DTYPE_BF16 ? 2 : 1;
     void *out = static_cast<char *>(a.out) + row * a.ldo * OB;
+    bool overflow = false;  // an output of this thread is not finite
     auto finish = [&](uint32_t at, float(&t)[kChunk]) {
         if constexpr (OP == NORM)
-            for (uint32_t i = 0; i < kChunk; ++i) t[i] *= factor;
+            for (uint32_t i = 0; i < kChunk; ++i) {
+                t[i] *= factor;
+                if constexpr (OUT == EQ_DTYPE_BF16) overflow |= !(fabsf(t[i]) < __builtin_inff());
+            }
         store8<OUT>(out, at, t, inv);
     };
-    if constexpr (NV > 0) {
+    auto finish1 = [&](uint32_t at, float t) {
+        if constexpr (OP == NORM) {
+            t *= factor;
+            if constexpr (OUT == EQ_DTYPE_BF16) overflow |= !(fabsf(t) < __builtin_inff());
+        }
+        store1<OUT>(out, at, t, inv);
+    };
+    if (NV > 0 && !twice) {
 #pragma unroll
         for (int i = 0; i < NV; ++i)
             if (first + i * step < whole) finish(first + i * step, v[i]);
-    } else {
-        // a norm's second pass reads back what this thread itself stored
-        typedef Row<OP, RES ? RES == EQ_DTYPE_F32 : XF32, 0> Again;
-        RowArgs b = a;
-        if constexpr (RES != 0) {
-            b.x = a.r_out;
-            b.ldx = a.ldro;
-        }
-        const Again again(b, row);
-        for (uint64_t at = first; at < whole; at += step) {
-            again.values8((uint32_t)at, v[0], sum, top);
-            finish((uint32_t)at, v[0]);
-        }
+        if (extra) finish1(last, v1);
+        twice = overflow;
     }
-    if (extra) store1<OUT>(out, last, OP == NORM ? v1 * factor : v1, inv);
+    if constexpr (NV == 0 || OP == NORM) {
+        if (!twice) return;
+        float sum2 = 0.0f;
+        uint32_t top2 = 0;
+        if constexpr (OP == NORM && OUT == EQ_DTYPE_BF16)  // finished
+            read_again([] { return FINAL; }, k, factor, sum2, top2,
+                       [&](uint32_t at, float(&t)[kChunk]) { store8_bf16(out, at, t); },
+                       [&](uint32_t at, float t) { store1<OUT>(out, at, t, 1.0f); });
+        else
+            read_again([] { return SCALED; }, k, 1.0f, sum2, top2, finish, finish1);
+    }
 }
 
 typedef void (*RowFn)(RowArgs);
