@@ -57,6 +57,10 @@ struct W4Args {
     uint32_t rows, cols;
     uint32_t k_tiles, row_tiles;  // columns and rows of tiles
     uint32_t kw_log2;             // 1 << kw_log2 waves share out the columns (k_w4)
+    // a wave's rows of tiles: the kernel's R, or 1 where there are fewer than R (it
+    // then computes that one R times and stores it once), and the step from one
+    // to the next in tiles
+    uint32_t wave_tiles, r_step;
     uint32_t group;
 };
 
@@ -282,10 +286,10 @@ struct Weights {
 
     // tile0: the first of the wave's rows of tiles, lane offsets apart from it
     // (a uniform base in scalar registers and one 32-bit offset per lane)
-    __device__ __forceinline__ void load(const W4Args &T, uint64_t tile0, uint32_t kt, uint32_t k_tiles, uint32_t lane) {
+    __device__ __forceinline__ void load(const W4Args &T, uint64_t tile0, uint32_t kt, uint32_t r_step, uint32_t lane) {
 #pragma unroll
         for (int r = 0; r < R; ++r) {
-            const uint64_t tile = tile0 + (uint64_t)r * k_tiles + kt;
+            const uint64_t tile = tile0 + (uint64_t)r * r_step + kt;
             c[r] = __builtin_nontemporal_load(T.codes + tile * 64 + lane);  // read once: plain loads took 8% longer
             const uint16_t *sp = T.scales + tile * 16 * P + (lane & 15u) * P;
             if constexpr (P == 1) s[r][0] = *sp;
@@ -433,7 +437,8 @@ __global__ void __launch_bounds__(64 * kWaves) k_w4(W4Launch a) {
     const uint32_t kw_n = 1u << T.kw_log2, rw_n = kWaves >> T.kw_log2;
     const uint32_t rw = wave >> T.kw_log2, kw = wave & (kw_n - 1);
     const uint32_t row_tiles = T.row_tiles, k_tiles = T.k_tiles, k_full = T.cols / kTileCols;
-    const uint32_t wg_tile = (blockIdx.x - a.wg_begin[ti]) * rw_n * R;
+    const uint32_t wave_tiles = T.wave_tiles, r_step = T.r_step;
+    const uint32_t wg_tile = (blockIdx.x - a.wg_begin[ti]) * rw_n * wave_tiles;
     const uint32_t token0 = blockIdx.y * a.per_pass;
 
     const char *x_row[NT];
@@ -445,10 +450,10 @@ __global__ void __launch_bounds__(64 * kWaves) k_w4(W4Launch a) {
     }
     uint32_t x_col[NL];
     for (uint32_t l = 0; l < NL; ++l) x_col[l] = K::col(load_quarter, l * LJ + load_row % LJ);
-    // rows of tiles past the end: the wave computes its R rows from the last
-    // R that exist (R <= row_tiles, see the launcher), stores skip them
-    uint32_t tile0 = wg_tile + rw * R;
-    tile0 = tile0 + R <= row_tiles ? tile0 : row_tiles - R;
+    // rows of tiles past the end: the wave computes its rows from the last ones
+    // that exist (wave_tiles <= row_tiles, see the launcher), stores skip them
+    uint32_t tile0 = wg_tile + rw * wave_tiles;
+    tile0 = tile0 + wave_tiles <= row_tiles ? tile0 : row_tiles - wave_tiles;
     const uint64_t base = (uint64_t)tile0 * k_tiles;
 
     struct St {  // what the wave reads of one column of tiles
@@ -456,14 +461,14 @@ __global__ void __launch_bounds__(64 * kWaves) k_w4(W4Launch a) {
         typename K::Raw x[NT][NL];
     };
     auto load = [&](St &st, uint32_t kt) {
-        st.w.load(T, base, kt, k_tiles, lane);
+        st.w.load(T, base, kt, r_step, lane);
 #pragma unroll
         for (int n = 0; n < NT; ++n)
             for (uint32_t l = 0; l < NL; ++l)
                 st.x[n][l] = load_raw<X, typename K::Raw>(x_row[n] + ((uint64_t)kt * kTileCols + x_col[l]) * XB);
     };
     auto load_tail = [&](St &st, uint32_t kt) {
-        st.w.load(T, base, kt, k_tiles, lane);
+        st.w.load(T, base, kt, r_step, lane);
 #pragma unroll
         for (int n = 0; n < NT; ++n)
             for (uint32_t l = 0; l < NL; ++l)
@@ -546,9 +551,10 @@ __global__ void __launch_bounds__(64 * kWaves) k_w4(W4Launch a) {
     // the row of tiles of the workgroup's o-th output, none where it is another's
     constexpr uint32_t kNone = ~0u;
     auto row_tile_of = [&](uint32_t o) -> uint32_t {
-        const uint32_t r = o % R, t0 = wg_tile + o / R * R;
-        if (t0 + R <= row_tiles) return t0 + r;
-        return t0 >= row_tiles || row_tiles - R + r < t0 ? kNone : row_tiles - R + r;
+        const uint32_t r = o % R, t0 = wg_tile + o / R * wave_tiles;
+        if (r >= wave_tiles || t0 >= row_tiles) return kNone;
+        if (t0 + wave_tiles <= row_tiles) return t0 + r;
+        return row_tiles - wave_tiles + r < t0 ? kNone : row_tiles - wave_tiles + r;
     };
     bool bad = false;
 #pragma unroll
@@ -601,8 +607,11 @@ __global__ void __launch_bounds__(64 * kWaves) k_w4(W4Launch a) {
 // matrix instruction hides only about two.
 constexpr uint32_t kChunkTiles = 4;
 
+// (E2M1 x bf16 with two token tiles fits twice on a compute unit with 128
+// registers; left alone the compiler takes 128 or 130.)
 template <uint32_t W, uint32_t X, uint32_t S, bool Z, int NT, int R>
-__global__ void __launch_bounds__(64 * kWaves) k_w4_wide(W4Launch a) {
+__global__ void __launch_bounds__(64 * kWaves, W == EQ_DTYPE_E2M1 && X == EQ_DTYPE_BF16 && NT == 2 ? 4 : 2)
+k_w4_wide(W4Launch a) {
     // KS: how a lane loads activations; K: how it multiplies
     typedef Kind<W, X, S, Z> KS;
     typedef Kind<W, X == EQ_DTYPE_E4M3 ? EQ_DTYPE_BF16 : X, S, Z> K;
@@ -624,8 +633,9 @@ __global__ void __launch_bounds__(64 * kWaves) k_w4_wide(W4Launch a) {
     const uint32_t row_tiles = T.row_tiles, k_tiles = T.k_tiles;
     const uint32_t chunks = T.cols / (C * kTileCols);  // whole ones
     const uint32_t token0 = blockIdx.y * a.per_pass;
-    const uint32_t want = ((blockIdx.x - a.wg_begin[ti]) * kWaves + wave) * R;  // as in k_w4
-    const uint32_t tile0 = want + R <= row_tiles ? want : row_tiles - R;
+    const uint32_t wave_tiles = T.wave_tiles, r_step = T.r_step;
+    const uint32_t want = ((blockIdx.x - a.wg_begin[ti]) * kWaves + wave) * wave_tiles;  // as in k_w4
+    const uint32_t tile0 = want + wave_tiles <= row_tiles ? want : row_tiles - wave_tiles;
     const uint64_t base = (uint64_t)tile0 * k_tiles;
 
     // the wave's loads of a chunk: (tile, token tile, piece) triples, in the
@@ -711,7 +721,7 @@ __global__ void __launch_bounds__(64 * kWaves) k_w4_wide(W4Launch a) {
 
     Weights<S, Z, R> w[C];
     const uint32_t ragged = chunks * C;  // first column of tiles of the last, short chunk
-    auto load_w = [&](Weights<S, Z, R> &d, uint32_t kt) { d.load(T, base, kt < k_tiles ? kt : k_tiles - 1, k_tiles, lane); };
+    auto load_w = [&](Weights<S, Z, R> &d, uint32_t kt) { d.load(T, base, kt < k_tiles ? kt : k_tiles - 1, r_step, lane); };
 #pragma unroll
     for (uint32_t d = 0; d < C; ++d) load_w(w[d], d);
     if (chunks) {
@@ -751,7 +761,7 @@ __global__ void __launch_bounds__(64 * kWaves) k_w4_wide(W4Launch a) {
 #pragma unroll
     for (int r = 0; r < R; ++r) {
         const uint32_t row = (tile0 + r) * kTileRows + i16;
-        if (tile0 + r < want || row >= T.rows) continue;  // another wave's row of tiles, or none
+        if (r >= (int)wave_tiles || tile0 + r < want || row >= T.rows) continue;  // another wave's row of tiles, or none
 #pragma unroll
         for (int n = 0; n < NT; ++n)
             for (int i = 0; i < 4; ++i) {
@@ -768,7 +778,7 @@ __global__ void __launch_bounds__(64 * kWaves) k_w4_wide(W4Launch a) {
             __threadfence_block();  // lanes read what others of the wave stored
             const uint32_t end = token0 + 16 * NT < a.tokens ? token0 + 16 * NT : a.tokens;
 #pragma unroll 1
-            for (uint32_t r = 0; r < R; ++r) {
+            for (uint32_t r = 0; r < wave_tiles; ++r) {
                 if (tile0 + r < want) continue;
 #pragma unroll 1
                 for (uint32_t t = token0; t < end; ++t) sum_again<W, S, Z>(T, a.y_f32, t, tile0 + r);
@@ -907,15 +917,15 @@ struct Shape {
 //    spread over passes of 32 or 16 (64 tokens int8 x 1024 x 8192: 6.4, one pass
 //    14.4; bf16 x 4096 x 4096: 10.1, 15.4; 1024 instead of 512: 8192 x 28672 int8
 //    63.8 against 48.9).
-Shape shape(uint64_t tokens, uint64_t row_tiles, uint64_t fewest, uint32_t kw_log2) {
+Shape shape(uint64_t tokens, uint64_t row_tiles, uint32_t kw_log2) {
     uint32_t nt = tokens <= 16 ? 1 : tokens <= 32 ? 2 : 4;
     const uint32_t tp = tokens <= 4 ? 4 : tokens <= 8 ? 8 : 16;
-    if (tokens > 8 && fewest >= 2 && row_tiles >= (nt == 1 ? 2560 : nt == 2 ? 1536 : 1024))
+    if (tokens > 8 && row_tiles >= (nt == 1 ? 2560 : nt == 2 ? 1536 : 1024))
         return {nt, tp, row_tiles >= 2560 ? 2u : 1u, true};
     const uint64_t wgs = ((row_tiles << kw_log2) + kWaves - 1) / kWaves;  // with one row of tiles a wave
     while (nt > 1 && wgs * ((tokens + 16 * nt - 1) / (16 * nt)) < 512) nt /= 2;
     uint32_t r = tokens == 1 ? 1 : tokens <= 8 || nt == 4 || wgs < 640 ? 2 : 4;
-    while (r > 1 && (wgs < 128 * r || fewest < r)) r /= 2;
+    while (r > 1 && wgs < 128 * r) r /= 2;
     return {nt, tp, r, false};
 }
 
@@ -986,18 +996,16 @@ eq_status eq_w4_matvec(const eq_w4_tensor *tensors, uint32_t n_tensors, const eq
         for (uint32_t i = 0; i < first; ++i) before += kind(i) == kind(first);
         if (before % EQ_MAX_BLOCK_TENSORS) continue;
         uint32_t which[EQ_MAX_BLOCK_TENSORS], n = 0;
-        uint64_t total = 0, fewest = ~0ull;  // rows of tiles
+        uint64_t total = 0;  // rows of tiles
         uint32_t kw = 0;
         for (uint32_t i = first; i < n_tensors && n < EQ_MAX_BLOCK_TENSORS; ++i) {
             if (kind(i) != kind(first)) continue;
             which[n++] = i;
-            const uint64_t rt = (tensors[i].rows + kTileRows - 1) / kTileRows;
-            total += rt;
-            fewest = rt < fewest ? rt : fewest;
+            total += (tensors[i].rows + kTileRows - 1) / kTileRows;
             const uint32_t k = kw_log2((uint32_t)((tensors[i].cols + kTileCols - 1) / kTileCols));
             kw = k > kw ? k : kw;
         }
-        const Shape sh = shape(tokens, total, fewest, kw);
+        const Shape sh = shape(tokens, total, kw);
         W4Launch a{};
         uint64_t wgs = 0;
         for (uint32_t k = 0; k < EQ_MAX_BLOCK_TENSORS; ++k) a.wg_begin[k] = ~0u;
@@ -1012,7 +1020,9 @@ eq_status eq_w4_matvec(const eq_w4_tensor *tensors, uint32_t n_tensors, const eq
             t.ldy = y[i].stride;
             a.wg_begin[k] = (uint32_t)wgs;
             t.kw_log2 = sh.wide ? 0 : kw_log2(t.k_tiles);
-            const uint64_t per_wg = (kWaves >> t.kw_log2) * sh.r;
+            t.wave_tiles = t.row_tiles < sh.r ? 1 : sh.r;
+            t.r_step = t.wave_tiles == 1 ? 0 : t.k_tiles;
+            const uint64_t per_wg = (kWaves >> t.kw_log2) * t.wave_tiles;
             wgs += (t.row_tiles + per_wg - 1) / per_wg;
         }
         a.per_pass = sh.tp < 16 ? kMaxTokens : 16 * sh.nt;
