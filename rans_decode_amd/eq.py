@@ -355,6 +355,21 @@ def _raw_stream():
         lambda index: torch.cuda.current_stream(index).cuda_stream)
 
 
+@functools.lru_cache(maxsize=None)
+def _current_gpu():
+    """The current device's index (without torch.cuda.current_device's own checks: a call's
+    tensors are on a GPU)."""
+    torch = _torch()
+    return getattr(torch._C, "_cuda_getDevice", None) or torch.cuda.current_device
+
+
+def _gpu_of(name: str, t) -> int:
+    gpu = t.get_device()
+    if gpu < 0:
+        raise ValueError(f"{name}: must be on the GPU")
+    return gpu
+
+
 def _enqueue(name: str, gpu: int, stream, *args) -> None:
     """The library's call `name` on GPU `gpu` and one of its streams (None: its
     current one). The GPU is made the current one for the call: kernels are
@@ -367,12 +382,13 @@ def _enqueue(name: str, gpu: int, stream, *args) -> None:
         if on is not None and on != gpu:
             raise ValueError(f"{name}: a stream of cuda:{on}, tensors on cuda:{gpu}")
         handle = _stream_handle(stream)
-    cuda = _torch().cuda
-    if cuda.current_device() == gpu:
-        _check(name, getattr(_lib, name)(*args, handle))
+    if _current_gpu()() == gpu:
+        status = getattr(_lib, name)(*args, handle)
     else:
-        with cuda.device(gpu):
-            _check(name, getattr(_lib, name)(*args, handle))
+        with _torch().cuda.device(gpu):
+            status = getattr(_lib, name)(*args, handle)
+    if status:
+        _check(name, status)
 
 
 def _matrix(name: str, t, gpu: int, tokens: int, cols: int, scale=None) -> bytes:
@@ -384,10 +400,8 @@ def _matrix(name: str, t, gpu: int, tokens: int, cols: int, scale=None) -> bytes
         raise ValueError(f"{name}: expected [{tokens}, {cols}], got {tuple(t.shape)}")
     if stride[-1] != 1 and cols > 1:
         raise ValueError(f"{name}: elements of a row must be contiguous")
-    if not t.is_cuda:
-        raise ValueError(f"{name}: must be on the GPU")
     if t.get_device() != gpu:
-        raise ValueError(f"{name}: on cuda:{t.get_device()}, other tensors of the call on cuda:{gpu}")
+        raise ValueError(f"{name}: on {t.device}, other tensors of the call on cuda:{gpu}")
     ld = stride[0] if tokens > 1 else cols  # one row has any stride
     if dtype == EQ_DTYPE_F32 or dtype == EQ_DTYPE_BF16:
         if scale is not None:
@@ -413,7 +427,7 @@ def eq_add_rmsnorm(x, weight, eps: float, out, out_scale=None, residual=None, re
     (default: into residual itself). out: bfloat16, or int8 / float8_e4m3fn
     with out_scale (fp32, one per token). weight: bf16 or fp32 [cols], or None."""
     tokens, cols = _size(x)
-    gpu = x.get_device()
+    gpu = _gpu_of("x", x)
     r = ro = w = None
     w_type = 0
     if residual is not None:
@@ -423,8 +437,7 @@ def eq_add_rmsnorm(x, weight, eps: float, out, out_scale=None, residual=None, re
         raise ValueError("residual_out without a residual")
     if weight is not None:
         w_type = _activation_type(weight.dtype)
-        if weight.numel() != cols or not weight.is_contiguous() or not weight.is_cuda \
-                or weight.get_device() != gpu:
+        if weight.numel() != cols or not weight.is_contiguous() or weight.get_device() != gpu:
             raise ValueError(f"weight: {cols} contiguous values on x's GPU")
         w = weight.data_ptr()
     _enqueue("eq_add_rmsnorm", gpu, stream, _matrix("x", x, gpu, tokens, cols), r, ro, w, w_type, eps, tokens, cols,
@@ -436,7 +449,7 @@ def eq_silu_mul(gate, up, out, out_scale=None, stream=None) -> None:
     bf16, rows may be strided: two halves of one buffer). out and out_scale as
     for eq_add_rmsnorm."""
     tokens, cols = _size(gate)
-    gpu = gate.get_device()
+    gpu = _gpu_of("gate", gate)
     _enqueue("eq_silu_mul", gpu, stream, _matrix("gate", gate, gpu, tokens, cols), _matrix("up", up, gpu, tokens, cols),
              tokens, cols, _matrix("out", out, gpu, tokens, cols, out_scale))
 
@@ -485,10 +498,13 @@ class W4Tensor:
 
 
 class W4Block:
-    """Tensors multiplied by one call (eq_w4_matvec). Keeps them alive."""
+    """Tensors multiplied by one call (eq_w4_matvec), all on one GPU. Keeps them alive."""
 
     def __init__(self, tensors):
         self.tensors = list(tensors)
+        self.gpu = self.tensors[0].gpu if self.tensors else None
+        if any(t.gpu != self.gpu for t in self.tensors):
+            raise ValueError("tensors of one block must be on one GPU")
         self.c = (eq_w4_tensor * max(1, len(self.tensors)))(*[t.c for t in self.tensors])
 
 
@@ -503,10 +519,7 @@ def eq_w4_matvec(block: W4Block, xs, ys, x_scales=None, stream=None) -> None:
         raise ValueError("one x, one y and, with scales, one x_scales entry per tensor")
     if n == 0:
         return
-    tokens, gpu = _size(xs[0])[0], xs[0].get_device()
-    for t in tensors:
-        if t.gpu != gpu:
-            raise ValueError(f"x on {xs[0].device}, weights on cuda:{t.gpu}")
+    tokens, gpu = _size(xs[0])[0], block.gpu
     xm = b"".join([_matrix("x", x, gpu, tokens, t.cols, x_scales[i] if x_scales is not None else None)
                    for i, (t, x) in enumerate(zip(tensors, xs))])
     ym = b"".join([_matrix("y", y, gpu, tokens, t.rows) for t, y in zip(tensors, ys)])

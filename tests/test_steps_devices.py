@@ -66,7 +66,7 @@ def gpus(monkeypatch):
     real = eq._lib
     monkeypatch.setattr(eq, "_lib", Library())
     monkeypatch.setattr(eq, "_raw_stream", lambda: lambda index: 40 + index)
-    monkeypatch.setattr(torch.cuda, "current_device", lambda: now[0])
+    monkeypatch.setattr(eq, "_current_gpu", lambda: lambda: now[0])
     monkeypatch.setattr(torch.cuda, "device", device)
     monkeypatch.setattr(torch, "empty", lambda *a, **k: Tensor(64, dtype=k["dtype"], gpu=k["device"].index)
                         if getattr(k.get("device"), "type", "") == "cuda" else empty(*a, **k))
