@@ -439,7 +439,7 @@ eq_status eq_add_rmsnorm(const eq_matrix *x, const eq_matrix *residual, const eq
 
 /*
  * eq_silu_mul -- per element: out = gate / (1 + exp(-gate)) * up, in fp32
- * (relative error below 8 * 2^-23 for every gate), rounded once. gate, up: F32 or BF16, both the same type (two halves of one
+ * (relative error below 9 * 2^-23 where it is a normal number), rounded once. gate, up: F32 or BF16, both the same type (two halves of one
  * buffer are two matrices with its stride). out: BF16, INT8 or E4M3; it must
  * not overlap the inputs.
  * Errors: EQ_EINVAL (as eq_add_rmsnorm), EQ_EHIP.

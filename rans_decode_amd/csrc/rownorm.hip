@@ -17,10 +17,11 @@
 //     floating-point maximum would drop.
 // What bounds both: HBM. One workgroup per row holds the row in registers in
 // chunks of 8 values per thread (16-byte loads of bf16), so nothing is read
-// twice. Measured: norm of 8192 x 8192 bf16 with a bf16 residual to E4M3 83.7 us,
-// 5.6 TB/s (a device copy: 5.1); silu of 4096 x 11008 bf16 to E4M3 44.3 us, 5.1
-// TB/s; one row of 4096 2.2 us, of 28672 (silu, fp32 to int8) 4.8: a launch and
-// the latency of one load, reduction and store.
+// twice. Measured (graph replays): norm of 8192 x 8192 bf16 with a bf16 residual
+// to E4M3 85.8 us, 5.5 TB/s (a device copy: 5.1); silu of 4096 x 11008 bf16 to
+// E4M3 44.6 us, 5.1 TB/s; one row of 4096 2.6 us, a launch and the latency of one
+// load, reduction and store; one row of 28672 (silu, fp32 to int8) 5.3, the
+// arithmetic of a row on one compute unit.
 #include <hip/hip_runtime.h>
 
 #include <cmath>
@@ -464,9 +465,10 @@ eq_status launch_rows(RowFn fn, const RowArgs &a, uint64_t tokens, uint32_t thre
 }
 
 // Threads per row and chunks per thread. Few rows: a thread per chunk (512 rows
-// of 4096: 5.2 us, with three chunks a thread 5.9); many: up to three, so that
-// more rows are on their way at once (8192 rows of 8192, bf16 with residual to
-// E4M3: 90.3 us, one chunk 95.3, four 106.1; 1777 rows of 5000: 9.6, one 10.8).
+// of 4096: 5.3 us, with three chunks a thread 5.8); many: up to three, so that
+// more rows are on their way at once (1777 rows of 5003 bf16: 11.3 us, one chunk
+// 14.9, two 13.8; of 5000 9.5, 12.1; 8192 rows of 8192 with residual to E4M3: 85.8,
+// one 84.7, four 88.8).
 void shape(uint64_t tokens, uint64_t cols, uint32_t *threads, int *nv) {
     const uint64_t chunks = (cols + kChunk - 1) / kChunk, most = tokens < 1024 ? 1 : 3;
     uint32_t t = 64;

@@ -21,12 +21,13 @@
 //     fp4 matrix instruction takes them as they are, but adds its 128 products
 //     with fewer than 32 bits: 1.0e-5 off in 2-norm over a row of 28672, where
 //     fp32 sums are 1e-7 off.)
-// What bounds it: at one token HBM reads of the codes (two 28672 x 8192 INT4
-// matrices, int8 activations: 36.7 us, 6.6 TB/s; bf16: 39.0); at 16 tokens over
-// few rows the activations, re-read from L2 by every workgroup (8192 x 28672
-// E2M1, E4M3: 23.9 us, 5.1 TB/s of codes); at 64 tokens the conversion and
-// scaling of the sums (the two matrices, int8: 57.7 us, 4.2 TB/s); small
-// matrices a launch and one memory latency (4096 x 4096, one token: 3.6 us).
+// What bounds it (graph replays over several copies of the weights): at one
+// token HBM reads of the codes (two 28672 x 8192 INT4 matrices, int8 activations:
+// 36.4 us, 6.6 TB/s; bf16: 37.8); at 16 tokens over few rows the activations,
+// re-read from L2 by every workgroup (8192 x 28672 E2M1, E4M3: 24.3 us, 5.0 TB/s
+// of codes); at 64 tokens reading the codes and computing alike, which hide each
+// other only in part (the two matrices, int8: 56 us, 4.3 TB/s; see k_w4_wide);
+// small matrices a launch and one memory latency (4096 x 4096, one token: 4.1 us).
 #include <hip/hip_runtime.h>
 
 #include <cstdint>
@@ -412,8 +413,9 @@ __device__ __forceinline__ void wave_order() {
 // TP = 16: a load whose neighbouring lanes read 16 different rows takes the
 // cache 64 look-ups, one whose 4 neighbours read 64 consecutive bytes 16; so
 // lanes load in that order, lane = 4 row + quarter, and swap through LDS (a
-// wave's own slots: no barrier). The slots are rotated so that neither side
-// meets bank conflicts.
+// wave's own slots: no barrier). The slots are rotated by 4 per quarter; with
+// 16-byte pieces that does not free both sides of bank conflicts (counted: 1.4e6
+// cycles, 2.2 us a compute unit, in the 24.3 us of 16 tokens E4M3 x 8192 x 28672).
 template <uint32_t W, uint32_t X, uint32_t S, bool Z, int TP, int NT, int R, int D>
 __global__ void __launch_bounds__(64 * kWaves) k_w4(W4Launch a) {
     typedef Kind<W, X, S, Z> K;
@@ -600,11 +602,14 @@ __global__ void __launch_bounds__(64 * kWaves) k_w4(W4Launch a) {
 // each, share them: a chunk of kChunkTiles columns of tiles is put in LDS as
 // matrix operands while the chunk before it is computed (two buffers, one
 // barrier a chunk), and the codes of a whole chunk are on their way.
-// Measured, two 28672 x 8192 INT4 matrices, group 128, 64 tokens int8: 57.7 us
-// (k_w4 112); its loads alone take 55, its products and activations 45, the
-// products alone 41: per chunk and wave 64 matrix instructions and about 440
-// vector ones (a conversion and a multiply-add per sum and group), of which a
-// matrix instruction hides only about two.
+// Measured, two 28672 x 8192 INT4 matrices, group 128, 64 tokens int8: 55 to 58
+// us (k_w4 114). With the rest of the loop left out: loads of codes and scales 51
+// (with those of the activations 49), products and activations 48, products
+// alone 43. Each is most of the whole, and the one workgroup that a compute unit
+// holds by its registers (224 for 256 units) overlaps them only in part. Per chunk
+// and wave 64 matrix instructions and about 440 vector ones (a conversion and a
+// multiply-add per sum and group), of which a matrix instruction hides only about
+// two; the swap's bank conflicts are 4.6e6 cycles, 7.6 us a unit.
 constexpr uint32_t kChunkTiles = 4;
 
 // (E2M1 x bf16 with two token tiles fits twice on a compute unit with 128
@@ -900,23 +905,29 @@ struct Shape {
     bool wide;           // k_w4_wide
 };
 
-// Measured on MI355X (graph replays, us; rows of tiles of 16 rows):
+// Measured on MI355X (graph replays, us; rows of tiles of 16 rows), the rule's
+// choice first:
 //  * rows of tiles a wave takes (r), whose activations are loaded once: one
-//    token 1 (its activations are small: 4096 x 4096 3.6, with two 5.5); 2 to 8
-//    tokens 2 (gate + up 57344 x 8192, four tokens bf16 41.3, one 47.0; eight
-//    tokens 46.9, one 62.0); 9 to 32 tokens 4 where 160 workgroups remain
-//    (11008 x 4096, 16 tokens bf16 9.7, two 12.3) and 2 below (8192 x 28672
-//    E4M3 26.5, four 37.1); 33 to 64 tokens 2 (registers). Halved while fewer
-//    than 128 workgroups would remain.
+//    token 1 (its activations are small: 4096 x 4096 4.2, two 5.0); 2 to 8
+//    tokens 2 (gate + up 57344 x 8192, four tokens bf16 38.2, one 43.0; eight
+//    tokens 43.0, one 58.6; 5001 x 4133 with zeros, seven tokens 7.0, one 8.6); 9 to 32
+//    tokens 4 where 160 workgroups remain (11008 x 4096, 16 tokens bf16 9.0, two
+//    10.2) and 2 below (8192 x 28672 E4M3 24.3, four 32.4); 33 to 64 tokens 2
+//    (registers: four would spill; INT4 with zeros in groups of 32 spills 6 at two
+//    and is still ahead, 11008 x 4096 36.9, one 42.2). Halved while fewer than 128
+//    workgroups would remain.
 //  * k_w4_wide where its workgroups of 8 r rows of tiles still fill the chip:
-//    16 tokens from 2560 rows of tiles (3584: bf16 49.1, k_w4 54.5; 1792: int8
-//    28.3, k_w4 25.8), 32 from 1536 (3584: int8 48.0, k_w4 58.6; 1280: 37.4,
-//    36.9), 64 from 1024 (3584: int8 57.5, k_w4 112; 688: bf16 33.0, 29.7);
-//    there r = 2 from 2560 (3584, 64 tokens int8: 62, one 69; 1792: 51, 41).
+//    16 tokens from 2560 rows of tiles (3584: bf16 44.0, k_w4 55.8; 1792: int8
+//    25.2, wide 29.1), 32 from 1536 (3584: int8 47.8, k_w4 57.8), 64 from 1024
+//    (3584: int8 55.3, k_w4 114; 688: bf16 30.2, wide 32.3); there r = 2 from 2560
+//    (3584, 64 tokens int8: 55.3, one 60.2; 1792: 36.0, two 47.6).
 //  * with fewer than 512 workgroups of one row of tiles a wave, the tokens are
 //    spread over passes of 32 or 16 (64 tokens int8 x 1024 x 8192: 6.4, one pass
-//    14.4; bf16 x 4096 x 4096: 10.1, 15.4; 1024 instead of 512: 8192 x 28672 int8
-//    63.8 against 48.9).
+//    14.7; bf16 x 4096 x 4096: 9.9, 15.9).
+// Where the rule takes the slower side: 4 tokens with r = 2 at 256 and 640 rows of
+// tiles (4096 x 4096 5.0, one 4.5; 10240 x 8192 E2M1 12.4, one 11.5); 32 tokens of
+// 8 bits at 1280 (28.9, wide 23.5); 64 tokens int8 x 8192 x 28672 in one pass
+// (47.3; two passes of r = 4 40.5).
 Shape shape(uint64_t tokens, uint64_t row_tiles, uint32_t kw_log2) {
     uint32_t nt = tokens <= 16 ? 1 : tokens <= 32 ? 2 : 4;
     const uint32_t tp = tokens <= 4 ? 4 : tokens <= 8 ? 8 : 16;
