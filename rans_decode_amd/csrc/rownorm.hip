@@ -189,12 +189,14 @@ __device__ __forceinline__ float silu(float g) { return fabsf(g) < kNear ? silu_
 
 // Whether a norm's sums can be used: squares overflow from |s| of 2^64 on, below
 // 2^-63 they lose bits (which matters where eps does not cover them), and s * w
-// may overflow although s * R * w does not. A row out of range is summed again
-// times 2^-80 or 2^80, a factor that R takes back: with 2^-80 up to 2^31 squares
-// of the largest s stay below 2^128. (Infinities and NaN come out the same.)
-// bf16 outputs need no maximum over the row: a thread that stored an infinity
-// takes (s * R) * w instead. (Looked for ahead of the reduction it cost 18
-// registers and 1777 rows of 5003 29%.)
+// may overflow although s * R * w does not. A row whose mean is out of range is
+// summed again times k = 2^-80 or 2^80, which R takes back: with 2^-80 up to 2^31
+// squares of the largest s stay below 2^128. (Infinities and NaN come out the
+// same.) The outputs of such a row, and of one where s * w overflowed, are (s * R) * w,
+// and so is what their 8-bit scale's maximum is taken of. bf16 outputs need no
+// maximum over the row: there a thread that stored an infinity looks again by itself.
+// (Looked for ahead of the reduction it cost 18 registers and 1777 rows of 5003
+// 29%.)
 constexpr float kMeanLow = 0x1p-90f, kMeanHigh = 0x1p126f, kRescale = 0x1p80f;
 constexpr uint32_t kInf = 0x7F800000u;
 
@@ -355,27 +357,38 @@ k_row(RowArgs a) {
     };
 
     float factor = 1.0f, inv = 1.0f, k = 1.0f;
-    bool twice = NV == 0;  // whether the output takes a second reading
+    bool again = false;  // the outputs are (s * k * factor) * w, read a second time
     if constexpr (OP == NORM || OUT != EQ_DTYPE_BF16) {
         reduce(sum, top, lds_sum, lds_top);
         if constexpr (OP == NORM) {
             float mean = sum / (float)a.cols + a.eps;
-            const bool in_range = mean >= kMeanLow && mean <= kMeanHigh && (OUT == EQ_DTYPE_BF16 || top < kInf);
-            if (!__builtin_amdgcn_readfirstlane(in_range)) {  // the same in all threads
-                k = mean < kMeanLow ? kRescale : 1.0f / kRescale;
-                sum = 0.0f;
-                top = 0;
-                read_again([] { return SCALED; }, k, 1.0f, sum, top, [](uint32_t, float(&)[kChunk]) {}, [](uint32_t, float) {});
-                __syncthreads();  // the first sums have been read
-                reduce(sum, top, lds_sum, lds_top);
-                mean = sum / (float)a.cols + a.eps * k * k;
-                twice = true;
-            }
+            const bool usable = mean >= kMeanLow && mean <= kMeanHigh;
             factor = rsqrtf(mean);
+            again = __builtin_amdgcn_readfirstlane(!usable || (OUT != EQ_DTYPE_BF16 && top >= kInf));  // the same in all threads
+            if (again) {
+                auto none = [](uint32_t, float(&)[kChunk]) {};
+                auto none1 = [](uint32_t, float) {};
+                if (!usable) {
+                    k = mean < kMeanLow ? kRescale : 1.0f / kRescale;
+                    sum = 0.0f;
+                    uint32_t unused = 0;
+                    read_again([] { return SCALED; }, k, 1.0f, sum, unused, none, none1);
+                    __syncthreads();  // the sums before have been read
+                    reduce(sum, unused, lds_sum, lds_top);
+                    mean = sum / (float)a.cols + a.eps * k * k;
+                    factor = rsqrtf(mean);
+                }
+                if constexpr (OUT != EQ_DTYPE_BF16) {
+                    top = 0;
+                    read_again([] { return FINAL; }, k, factor, sum, top, none, none1);
+                    __syncthreads();
+                    reduce(sum, top, lds_sum, lds_top);
+                }
+            }
         }
         if constexpr (OUT != EQ_DTYPE_BF16) {
             constexpr float L = OUT == EQ_DTYPE_INT8 ? 127.0f : 448.0f;
-            float amax = __uint_as_float(top) * factor;
+            float amax = again ? __uint_as_float(top) : __uint_as_float(top) * factor;
             amax = amax < kAmaxFloor ? kAmaxFloor : amax;  // a NaN stays
             inv = L / amax;
             if (threadIdx.x == 0) a.scale[row] = amax / L;
@@ -399,24 +412,24 @@ k_row(RowArgs a) {
         }
         store1<OUT>(out, at, t, inv);
     };
-    if (NV > 0 && !twice) {
+    float sum2 = 0.0f;
+    uint32_t top2 = 0;
+    if (!again) {
+        if constexpr (NV > 0) {
 #pragma unroll
-        for (int i = 0; i < NV; ++i)
-            if (first + i * step < whole) finish(first + i * step, v[i]);
-        if (extra) finish1(last, v1);
-        twice = overflow;
+            for (int i = 0; i < NV; ++i)
+                if (first + i * step < whole) finish(first + i * step, v[i]);
+            if (extra) finish1(last, v1);
+        } else {
+            read_again([] { return UNSCALED; }, 1.0f, 1.0f, sum2, top2, finish, finish1);
+        }
+        again = overflow;
     }
-    if constexpr (NV == 0 || OP == NORM) {
-        if (!twice) return;
-        float sum2 = 0.0f;
-        uint32_t top2 = 0;
-        if constexpr (OP == NORM && OUT == EQ_DTYPE_BF16)  // finished
+    if constexpr (OP == NORM)
+        if (again)
             read_again([] { return FINAL; }, k, factor, sum2, top2,
-                       [&](uint32_t at, float(&t)[kChunk]) { store8_bf16(out, at, t); },
-                       [&](uint32_t at, float t) { store1<OUT>(out, at, t, 1.0f); });
-        else
-            read_again([] { return SCALED; }, k, 1.0f, sum2, top2, finish, finish1);
-    }
+                       [&](uint32_t at, float(&t)[kChunk]) { store8<OUT>(out, at, t, inv); },
+                       [&](uint32_t at, float t) { store1<OUT>(out, at, t, inv); });
 }
 
 typedef void (*RowFn)(RowArgs);

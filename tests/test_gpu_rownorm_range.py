@@ -65,3 +65,14 @@ def test_products_with_the_weight_out_of_range(out):
         run(4, cols, 3e38, F32, None, out, eps=1e-5)
         run(4, cols, 1e15, F32, None, out, eps=1e-5, weight_size=1e25)
         run(4, cols, 1e10, BF16, BF16, out, eps=1e-5, weight_size=1e30, wt=BF16)
+
+
+@pytest.mark.parametrize("out", [BF16, I8, E4M3])
+def test_huge_weights(out):
+    """s * weight overflows where s itself is of ordinary size, and where s is small and eps 0."""
+    for cols in (7, 100, 4096, 20000, 33000):
+        run(4, cols, 100.0, F32, None, out, eps=1e-5, weight_size=5e37)
+        run(4, cols, 30.0, BF16, BF16, out, eps=1e-5, weight_size=5e37, wt=BF16)
+        run(5, cols, 1e-14, F32, None, out, weight_size=1e30)
+        run(4, cols, 1e-20, BF16, F32, out, weight_size=5e37)
+        run(4, cols, 1e19, F32, F32, out, eps=1e-5, weight_size=5e37, in_place=True)
